@@ -93,6 +93,25 @@ class SdvSchedStats(ctypes.Structure):
                                                  "finished", "admitted")] + [("queued", c_int), ("free_pages", c_int), ("live", c_int)]
 
 
+SDV_CACHE_BF16, SDV_CACHE_E4M3 = 0, 1
+
+
+class SdvCacheConfig(ctypes.Structure):
+    _fields_ = [(n, c_int) for n in ("n_q", "n_kv", "head_dim", "page_size", "cache_format")] + [("rope_theta", c_float)]
+
+
+class SdvChunk(ctypes.Structure):
+    _fields_ = [("B", c_int), ("T", c_int), ("max_q", c_int), ("row_offsets", c_void_p), ("kv_lens", c_void_p),
+                ("kv_pool", c_void_p), ("kv_scales", c_void_p), ("num_pool_pages", c_int),
+                ("page_table", c_void_p), ("max_pages_per_seq", c_int), ("window", c_int)]
+
+
+class SdvAppendRows(ctypes.Structure):
+    _fields_ = [("k", c_void_p), ("v", c_void_p), ("q", c_void_p),
+                ("k_stride", ctypes.c_longlong), ("v_stride", ctypes.c_longlong), ("q_stride", ctypes.c_longlong),
+                ("x_format", c_int), ("q_out", c_void_p), ("q_out_stride", ctypes.c_longlong)]
+
+
 TRACE_LIB_PATH = os.path.join(HERE, "libsdv_trace.so")
 _libs: dict = {}
 
@@ -150,6 +169,18 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.sdv_ngram_draft.argtypes = [P(c_int), c_int, c_int, c_int, c_int, P(c_int)]
     lib.sdv_ngram_draft_batch.restype = c_int
     lib.sdv_ngram_draft_batch.argtypes = [P(c_int), P(c_ll), c_int, c_int, c_int, c_int, P(c_int), P(c_int)]
+    lib.sdv_cache_workspace_size.restype = c_size_t
+    lib.sdv_cache_workspace_size.argtypes = [P(SdvCacheConfig), c_int, c_int]
+    lib.sdv_cache_create.restype = c_int
+    lib.sdv_cache_create.argtypes = [P(SdvCacheConfig), c_void_p, c_size_t, c_int, c_int, c_void_p, P(c_void_p)]
+    lib.sdv_cache_destroy.restype = None
+    lib.sdv_cache_destroy.argtypes = [c_void_p]
+    lib.sdv_cache_append.restype = c_int
+    lib.sdv_cache_append.argtypes = [c_void_p, P(SdvChunk), P(SdvAppendRows), c_void_p, c_void_p]
+    lib.sdv_cache_attention.restype = c_int
+    lib.sdv_cache_attention.argtypes = [c_void_p, P(SdvChunk), c_void_p, c_ll, c_void_p, c_ll, c_void_p, c_void_p]
+    lib.sdv_cache_read.restype = c_int
+    lib.sdv_cache_read.argtypes = [c_void_p, P(SdvChunk), c_void_p, c_ll, c_void_p, c_ll, c_int, c_void_p, c_void_p]
     lib.sdv_sched_gamma.restype = c_int
     lib.sdv_sched_gamma.argtypes = [c_int, c_int, c_int]
     lib.sdv_sched_create.restype = c_int

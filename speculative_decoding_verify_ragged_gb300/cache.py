@@ -1,0 +1,185 @@
+"""Python binding of the paged cache's operators (``include/sdv_cache.h``).
+
+Argument marshalling and checks only; the work runs in the library's kernels.
+
+Typical use, a chunk of new tokens through one layer::
+
+    cache = PagedCache(dict(n_q=32, n_kv=8, head_dim=128, cache_format="e4m3", rope_theta=1e6),
+                       max_rows=8192, max_slots=64)
+    pool, scales = cache.new_pool(pages)
+    chunk = cache.chunk(rows=T, max_q=longest, row_offsets=offsets, kv_lens=lens, page_table=table,
+                        kv_pool=pool, kv_scales=scales)
+    cache.append(chunk, k, v, status, q=q, q_out=q_rot)      # rotate, round, store
+    cache.attention(chunk, q_rot, out, status)               # over everything cached
+    cache.read(chunk, k_back, v_back, status)                # what the cache holds now
+
+A chunk keeps the addresses of its tensors; their contents (offsets, lengths,
+tables, pages) may change between calls, so one chunk serves a captured graph
+or a loop of steps.
+"""
+from __future__ import annotations
+
+import ctypes
+
+from . import SdvError, _ptr, _stream
+from ._abi import (SDV_CACHE_BF16, SDV_CACHE_E4M3, SDV_OK, SdvAppendRows, SdvCacheConfig, SdvChunk, load_library)
+
+__all__ = ["PagedCache", "Chunk"]
+
+FORMATS = {"bf16": SDV_CACHE_BF16, "e4m3": SDV_CACHE_E4M3}
+
+
+class Chunk:
+    """A ragged chunk's description (sdv_chunk) and the tensors that it points to."""
+
+    def __init__(self, struct: SdvChunk, tensors: tuple):
+        self.struct = struct
+        self.ref = ctypes.byref(struct)
+        self.rows = struct.T
+        self.tensors = tensors
+
+
+class PagedCache:
+    """Operators over a paged cache of one geometry, with their workspace.
+
+    cfg: n_q, n_kv, head_dim, page_size (16), cache_format ("bf16" or "e4m3"),
+    rope_theta (0 or absent: append does not rotate).  The workspace is
+    allocated here through torch, on the current device; calls of one
+    PagedCache must not overlap in time.
+    """
+
+    def __init__(self, cfg: dict, max_rows: int, max_slots: int, lib_path: str | None = None):
+        import torch
+        self.lib = load_library(lib_path) if lib_path else load_library()
+        fmt = cfg.get("cache_format", "bf16")
+        if fmt not in FORMATS:
+            raise ValueError(f"cache_format {fmt!r}: one of {sorted(FORMATS)}")
+        self.format = fmt
+        self.cfg = SdvCacheConfig(int(cfg["n_q"]), int(cfg["n_kv"]), int(cfg["head_dim"]),
+                                  int(cfg.get("page_size", 16)), FORMATS[fmt], float(cfg.get("rope_theta", 0.0)))
+        self.max_rows, self.max_slots = int(max_rows), int(max_slots)
+        nbytes = self.lib.sdv_cache_workspace_size(ctypes.byref(self.cfg), self.max_rows, self.max_slots)
+        if nbytes == 0:
+            raise SdvError(1, "sdv_cache_workspace_size rejected the configuration")
+        self.workspace = torch.empty(int(nbytes), dtype=torch.uint8, device="cuda")
+        self.device = self.workspace.device
+        h = ctypes.c_void_p()
+        self._check(self.lib.sdv_cache_create(ctypes.byref(self.cfg), _ptr(self.workspace), ctypes.c_size_t(nbytes),
+                                              self.max_rows, self.max_slots, _stream(None), ctypes.byref(h)),
+                    "sdv_cache_create")
+        self.handle = h
+
+    def close(self):
+        if getattr(self, "handle", None):
+            self.lib.sdv_cache_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    # -- marshalling -------------------------------------------------------
+
+    def _check(self, rc, what):
+        if rc != SDV_OK:
+            extra = f" (cuda error {self.lib.sdv_last_cuda_error()})" if rc == 4 else ""
+            raise SdvError(rc, what + extra)
+
+    def _want(self, t, name, dtype, shape=None):
+        if t.dtype != dtype:
+            raise ValueError(f"{name}: {t.dtype}, {dtype} is wanted")
+        if t.device != self.device:
+            raise ValueError(f"{name}: on {t.device}, the cache's operators run on {self.device}")
+        if shape is not None and (tuple(t.shape) != tuple(shape) or not t.is_contiguous()):
+            raise ValueError(f"{name}: shape {tuple(t.shape)} (contiguous: {t.is_contiguous()}), contiguous {tuple(shape)} is wanted")
+
+    def _rows(self, t, name, heads, rows, dtypes):
+        """The row stride of a [>= rows, heads, head_dim] tensor whose heads are contiguous."""
+        d = self.cfg.head_dim
+        if t.dtype not in dtypes:
+            raise ValueError(f"{name}: {t.dtype}, one of {dtypes} is wanted")
+        if t.device != self.device:
+            raise ValueError(f"{name}: on {t.device}, the cache's operators run on {self.device}")
+        s = t.shape
+        if len(s) != 3 or s[0] < rows or s[1] != heads or s[2] != d:
+            raise ValueError(f"{name}: shape {tuple(s)}, [{rows}, {heads}, {d}] is wanted")
+        st = t.stride()
+        if st[2] != 1 or (heads > 1 and st[1] != d):
+            raise ValueError(f"{name}: strides {tuple(st)}: a row's heads must be contiguous")
+        return st[0] if s[0] > 1 else max(st[0], heads * d)
+
+    def new_pool(self, pages: int):
+        """(kv_pool, kv_scales) of a cache of `pages` pages; kv_scales is None for bf16."""
+        import torch
+        shape = (int(pages), self.cfg.n_kv, 2, self.cfg.page_size, self.cfg.head_dim)
+        if self.format == "bf16":
+            return torch.zeros(shape, dtype=torch.bfloat16, device=self.device), None
+        return (torch.zeros(shape, dtype=torch.uint8, device=self.device),
+                torch.full(shape[:-1], 127, dtype=torch.uint8, device=self.device))
+
+    def chunk(self, rows: int, max_q: int, row_offsets, kv_lens, page_table, kv_pool, kv_scales=None,
+              window: int = 0) -> Chunk:
+        """Describe a ragged chunk (sdv_chunk): `rows` rows of at most `max_q` per sequence."""
+        import torch
+        B = int(kv_lens.shape[0])
+        self._want(kv_lens, "kv_lens", torch.int32, (B,))
+        self._want(row_offsets, "row_offsets", torch.int32, (B + 1,))
+        self._want(page_table, "page_table", torch.int32, (B, page_table.shape[-1]))
+        c = self.cfg
+        pool_shape = (kv_pool.shape[0], c.n_kv, 2, c.page_size, c.head_dim)
+        self._want(kv_pool, "kv_pool", torch.bfloat16 if self.format == "bf16" else torch.uint8, pool_shape)
+        if self.format == "e4m3":
+            if kv_scales is None:
+                raise ValueError("kv_scales: an e4m3 cache has them")
+            self._want(kv_scales, "kv_scales", torch.uint8, pool_shape[:-1])
+        elif kv_scales is not None:
+            raise ValueError("kv_scales: a bf16 cache has none")
+        s = SdvChunk(B, int(rows), int(max_q), row_offsets.data_ptr(), kv_lens.data_ptr(), kv_pool.data_ptr(),
+                     kv_scales.data_ptr() if kv_scales is not None else None, int(kv_pool.shape[0]),
+                     page_table.data_ptr(), int(page_table.shape[1]), int(window))
+        return Chunk(s, (row_offsets, kv_lens, page_table, kv_pool, kv_scales))
+
+    # -- entry points ------------------------------------------------------
+
+    def append(self, chunk: Chunk, k, v, status, q=None, q_out=None, stream=None):
+        """Store the chunk's k, v [T, n_kv, head_dim] (bf16 or fp32, rows strided), rotated where the cache
+        rotates; with q [T, n_q, head_dim] also its rotation in bf16 into q_out."""
+        import torch
+        self._want(status, "status", torch.int32)
+        c, T, io = self.cfg, chunk.rows, (k.dtype,)
+        ks = self._rows(k, "k", c.n_kv, T, (torch.bfloat16, torch.float32))
+        vs = self._rows(v, "v", c.n_kv, T, io)
+        if (q is None) != (q_out is None):
+            raise ValueError("q and q_out come together")
+        qs = self._rows(q, "q", c.n_q, T, io) if q is not None else 0
+        qos = self._rows(q_out, "q_out", c.n_q, T, (torch.bfloat16,)) if q is not None else 0
+        rows = SdvAppendRows(k.data_ptr(), v.data_ptr(), q.data_ptr() if q is not None else None, ks, vs, qs,
+                             1 if k.dtype == torch.float32 else 0, q_out.data_ptr() if q is not None else None, qos)
+        self._check(self.lib.sdv_cache_append(self.handle, chunk.ref, ctypes.byref(rows), _ptr(status), _stream(stream)),
+                    "sdv_cache_append")
+
+    def attention(self, chunk: Chunk, q, out, status, stream=None):
+        """Attention of q [T, n_q, head_dim] bf16 over the cached positions each row sees, into out."""
+        import torch
+        self._want(status, "status", torch.int32)
+        c, T, io = self.cfg, chunk.rows, (torch.bfloat16,)
+        qs, os_ = self._rows(q, "q", c.n_q, T, io), self._rows(out, "out", c.n_q, T, io)
+        self._check(self.lib.sdv_cache_attention(self.handle, chunk.ref, _ptr(q), qs, _ptr(out), os_, _ptr(status),
+                                                 _stream(stream)), "sdv_cache_attention")
+
+    def read(self, chunk: Chunk, k_out, v_out, status, stream=None):
+        """Read the chunk's positions back into k_out, v_out [T, n_kv, head_dim] (bf16 or fp32; either may be None)."""
+        import torch
+        self._want(status, "status", torch.int32)
+        c, T = self.cfg, chunk.rows
+        first = k_out if k_out is not None else v_out
+        if first is None:
+            raise ValueError("k_out, v_out: one of them is wanted")
+        io = (first.dtype,) if first.dtype in (torch.bfloat16, torch.float32) else (torch.bfloat16, torch.float32)
+        ks = self._rows(k_out, "k_out", c.n_kv, T, io) if k_out is not None else 0
+        vs = self._rows(v_out, "v_out", c.n_kv, T, io) if v_out is not None else 0
+        self._check(self.lib.sdv_cache_read(self.handle, chunk.ref, _ptr(k_out), ks, _ptr(v_out), vs,
+                                            1 if first.dtype == torch.float32 else 0, _ptr(status), _stream(stream)),
+                    "sdv_cache_read")

@@ -25,7 +25,7 @@ bool pdl_enabled() {
   return on;
 }
 
-static sdv_status cuda_fail(cudaError_t e) {
+sdv_status cuda_fail(cudaError_t e) {
   g_last_cuda_error = static_cast<int>(e);
   return SDV_ERR_CUDA;
 }

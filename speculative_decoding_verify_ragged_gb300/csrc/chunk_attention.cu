@@ -1,0 +1,471 @@
+// Attention of a ragged chunk over the paged cache, for few query rows per
+// sequence (mma.sync): softmax(q k^T / sqrt(d)) v with a running maximum and sum.
+//
+// An item is 16 packed query rows -- the n_q / n_kv heads of consecutive tokens
+// -- of one (sequence, key head) against its visible pages.  The items' pages
+// are laid end to end and cut into equal runs, one per block, so a single
+// long sequence and a batch of unlike ones load the GPU alike; an item cut
+// between blocks is joined by the last of them to arrive, in block order, so
+// equal inputs give equal bits.
+//
+// Within a block the four warps take pages in turn, straight from global memory
+// to registers: the sum over d of a score may run in any order, so a lane takes
+// 16 contiguous bytes of a key wherever the MMA wants its k index, and queries
+// are laid out to match; the columns of the output are likewise assigned so
+// that a lane's V loads are 16 contiguous bytes of four keys.  No value is
+// staged in shared memory.  e4m3 codes become fp16 exactly; a key's scale
+// multiplies its scores, a value's its weight.
+#include "chunk.cuh"
+
+namespace sdv {
+namespace {
+
+constexpr int CA_WARPS = 4;
+constexpr int CA_THREADS = CA_WARPS * kWarp;
+constexpr int ROWS = 16;          // packed query rows of an item
+constexpr float kNoMax = -1e30f;  // the maximum before the first visible key
+constexpr int kMinPages = 4;      // pages a block takes at least: one per warp
+constexpr int kSplitBias = 8;     // e4m3: weights carry 2^(e + 8), in fp16's normal range for every e
+
+constexpr int part_floats(int D) { return ROWS * (D + 2); }
+
+template <int D, int FMT>
+struct Frag {
+  static constexpr bool kCodes = FMT == SDV_CACHE_E4M3;
+  static constexpr int KSTEPS = D / 16;
+  static constexpr int ROW_BYTES = kCodes ? D : 2 * D;
+  static constexpr int KCH = ROW_BYTES / 64;                    // 16-byte chunks of a key row per lane (4 lanes a row)
+  static constexpr int VW = ROW_BYTES / 8 / 4;                  // words of a value row per lane (8 lanes a row)
+  static constexpr int NT = D / 8;                              // 8-column tiles of the output
+  uint32_t k[2][KCH * 4];  // keys g and g + 8
+  uint32_t v[4][VW];       // keys 2t, 2t + 1, 2t + 8, 2t + 9
+  uint32_t sc[2];          // e4m3: scale bytes of keys (2t, 2t + 1) and of (2t + 8, 2t + 9): K low half, V high half
+};
+
+// The output column of (lane group g of 8, tile j): the V words of a lane are contiguous.
+template <int D, int FMT>
+__device__ __forceinline__ int out_col(int g, int j) {
+  if constexpr (FMT == SDV_CACHE_E4M3) return g * (D / 8) + j;
+  return ((j >> 3) * 8 + g) * 8 + (j & 7);
+}
+
+// Cache loads are used once by this SM: kept out of L1.
+__device__ __forceinline__ uint4 load16(const uint4* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint2 load8(const uint2* p) {
+  uint2 v;
+  asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  return v;
+}
+
+template <int D, int FMT>
+__device__ __forceinline__ void load_page(Frag<D, FMT>& f, const ChunkParams& c, int page, int h, int g, int t) {
+  using F = Frag<D, FMT>;
+  const long long head = ((long long)page * c.n_kv + h) * 2 * kPage;
+  const uint8_t* kp = c.pool + head * F::ROW_BYTES;
+  const uint8_t* vp = kp + kPage * F::ROW_BYTES;
+#pragma unroll
+  for (int r = 0; r < 2; ++r)
+#pragma unroll
+    for (int i = 0; i < F::KCH; ++i) {
+      const uint4 w = load16(reinterpret_cast<const uint4*>(kp + (g + 8 * r) * F::ROW_BYTES + (i * 4 + t) * 16));
+      f.k[r][4 * i] = w.x, f.k[r][4 * i + 1] = w.y, f.k[r][4 * i + 2] = w.z, f.k[r][4 * i + 3] = w.w;
+    }
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const uint8_t* row = vp + (2 * t + (r & 1) + 8 * (r >> 1)) * F::ROW_BYTES;
+    if constexpr (F::VW == 2) {
+      const uint2 w = load8(reinterpret_cast<const uint2*>(row + g * 8));
+      f.v[r][0] = w.x, f.v[r][1] = w.y;
+    } else {
+#pragma unroll
+      for (int i = 0; i < F::VW / 4; ++i) {
+        const uint4 w = load16(reinterpret_cast<const uint4*>(row + (i * 8 + g) * 16));
+        f.v[r][4 * i] = w.x, f.v[r][4 * i + 1] = w.y, f.v[r][4 * i + 2] = w.z, f.v[r][4 * i + 3] = w.w;
+      }
+    }
+  }
+  if constexpr (F::kCodes) {
+    const uint8_t* s = c.scales + head;
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+      f.sc[r] = static_cast<uint32_t>(*reinterpret_cast<const unsigned short*>(s + 2 * t + 8 * r)) |
+                static_cast<uint32_t>(*reinterpret_cast<const unsigned short*>(s + kPage + 2 * t + 8 * r)) << 16;
+  }
+}
+
+template <int D, int FMT>
+__global__ void __launch_bounds__(CA_THREADS, 2) chunk_attn_kernel(const ChunkAttnParams p) {
+  using F = Frag<D, FMT>;
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  float* s_o = reinterpret_cast<float*>(smem_raw);                     // [warps][16][D]
+  float* s_ml = s_o + CA_WARPS * ROWS * D;                             // [warps][2][16]
+  long long* s_base = reinterpret_cast<long long*>(s_ml + CA_WARPS * 2 * ROWS);  // [B + 1] first unit of each sequence
+  int* s_off = reinterpret_cast<int*>(s_base + p.c.B + 1);
+  int* s_len = s_off + p.c.B + 1;
+  __shared__ long long s_scan[CA_WARPS];
+  __shared__ int s_last;
+
+  griddep_launch_dependents();
+  griddep_wait();
+  const int B = p.c.B, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  const int group = p.c.n_q / p.c.n_kv, window = p.c.window;
+  // a call that has failed already writes nothing, but still takes its part in
+  // the counting below, so that the counters end at zero whichever block saw it
+  const bool dead = read_status(p.c.status) != 0;
+  if (!load_chunk(p.c, s_off, s_len)) return;
+
+  // pages of each of a sequence's items (those that any of its rows sees), first page
+  auto seq_pages = [&](const SeqRows& s, int& lo) {
+    lo = window > 0 ? max(0, s.pos0 - window + 1) / kPage : 0;
+    return s.n > 0 ? max(1, (s.len + kPage - 1) / kPage - lo) : 0;
+  };
+  auto seq_tiles = [&](const SeqRows& s) { return (int)(((long long)s.n * group + ROWS - 1) / ROWS); };
+  {
+    const int per = (B + CA_THREADS - 1) / CA_THREADS, b0 = min(B, tid * per), b1 = min(B, b0 + per);
+    long long sum = 0;
+    for (int b = b0; b < b1; ++b) {
+      const SeqRows s = seq_rows(s_off, s_len, b);
+      int lo;
+      const int u = seq_pages(s, lo);
+      s_base[b] = sum;
+      sum += (long long)u * seq_tiles(s) * p.c.n_kv;
+    }
+    long long inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += v;
+    }
+    if (lane == 31) s_scan[warp] = inc;
+    __syncthreads();
+    long long add = inc - sum;
+    for (int w = 0; w < warp; ++w) add += s_scan[w];
+    for (int b = b0; b < b1; ++b) s_base[b] += add;
+    if (tid == CA_THREADS - 1) s_base[B] = add + sum;
+    __syncthreads();
+  }
+  const long long units = s_base[B];
+  const long long per_cta = max((long long)kMinPages, (units + gridDim.x - 1) / gridDim.x);
+  const long long u_end = min(units, (blockIdx.x + 1) * per_cta);
+
+  for (long long u = blockIdx.x * per_cta; u < u_end;) {
+    int b = 0;
+    {
+      int lo = 0, hi = B - 1;  // the last b with s_base[b] <= u (empty sequences share their successor's base)
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (s_base[mid] <= u) lo = mid;
+        else hi = mid - 1;
+      }
+      b = lo;
+    }
+    const SeqRows sq = seq_rows(s_off, s_len, b);
+    int lo_page;
+    const int n_pages = seq_pages(sq, lo_page), tiles = seq_tiles(sq);
+    const long long item = (u - s_base[b]) / n_pages;  // within the sequence: key head, then tile
+    const int page0 = static_cast<int>((u - s_base[b]) - item * n_pages);
+    const int h = static_cast<int>(item / tiles), row0 = static_cast<int>(item - (long long)h * tiles) * ROWS;
+    const int n_here = static_cast<int>(min(u_end - u, (long long)(n_pages - page0)));
+    const int n_rows = static_cast<int>(min((long long)ROWS, (long long)sq.n * group - row0));
+    const int pmin = sq.pos0 + row0 / group, pmax = sq.pos0 + (row0 + n_rows - 1) / group;
+    // pages of this run that a row of the item sees
+    const int first = max(lo_page + page0, window > 0 ? max(0, pmin - window + 1) / kPage : 0);
+    const int last = min(lo_page + page0 + n_here, pmax < 0 ? 0 : pmax / kPage + 1);
+
+    // queries: rows g and g + 8, laid out like the keys
+    uint32_t qf[F::KSTEPS][4];
+    int pos[2];
+    float cz[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int row = row0 + g + 8 * r;
+      const bool in = g + 8 * r < n_rows;
+      pos[r] = in ? sq.pos0 + row / group : -1;
+      const __nv_bfloat16* src =
+          p.q + (in ? (long long)(sq.off + row / group) * p.q_stride + (long long)(h * group + row % group) * D : 0);
+      cz[r] = p.scale_log2;
+      if constexpr (F::kCodes) {
+        // fp16 with the row's largest magnitude in [1/2, 1): what falls below
+        // 2^-25 of it is lost, far under the products' own rounding
+        uint2 w[F::KSTEPS];
+        float a = 0.f;
+#pragma unroll
+        for (int ks = 0; ks < F::KSTEPS; ++ks) {
+          w[ks] = in ? *reinterpret_cast<const uint2*>(src + (ks >> 2) * 64 + t * 16 + (ks & 3) * 4) : make_uint2(0u, 0u);
+          a = fmaxf(a, fmaxf(fmaxf(fabsf(__uint_as_float(w[ks].x << 16)), fabsf(__uint_as_float(w[ks].x & 0xFFFF0000u))),
+                             fmaxf(fabsf(__uint_as_float(w[ks].y << 16)), fabsf(__uint_as_float(w[ks].y & 0xFFFF0000u)))));
+        }
+        a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
+        a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
+        const int e = min(max(static_cast<int>(__float_as_uint(a) >> 23) - 126, -100), 100);
+        const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+        cz[r] *= __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+#pragma unroll
+        for (int ks = 0; ks < F::KSTEPS; ++ks) {
+          const __half2 x = __floats2half2_rn(__uint_as_float(w[ks].x << 16) * inv, __uint_as_float(w[ks].x & 0xFFFF0000u) * inv);
+          const __half2 y = __floats2half2_rn(__uint_as_float(w[ks].y << 16) * inv, __uint_as_float(w[ks].y & 0xFFFF0000u) * inv);
+          qf[ks][r] = *reinterpret_cast<const uint32_t*>(&x);
+          qf[ks][2 + r] = *reinterpret_cast<const uint32_t*>(&y);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < F::KCH; ++i) {
+          const uint4 w = in ? *reinterpret_cast<const uint4*>(src + (i * 4 + t) * 8) : make_uint4(0u, 0u, 0u, 0u);
+          qf[2 * i][r] = w.x, qf[2 * i][2 + r] = w.y, qf[2 * i + 1][r] = w.z, qf[2 * i + 1][2 + r] = w.w;
+        }
+      }
+    }
+
+    float o[F::NT][4];
+#pragma unroll
+    for (int j = 0; j < F::NT; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+    float m[2] = {kNoMax, kNoMax}, l[2] = {0.f, 0.f};
+
+    const int pg0 = first + warp;
+    const int mine = dead || pg0 >= last ? 0 : (last - pg0 + CA_WARPS - 1) / CA_WARPS;  // this warp's pages
+    int ids = 0;
+    Frag<D, FMT> nxt, cur;
+    auto page_id = [&](int i) {  // the warp's i-th page; the lanes fetch 32 ids at a time
+      if ((i & 31) == 0) {
+        ids = -1;
+        if (i + lane < mine) {
+          ids = p.c.page_table[(long long)b * p.c.max_pages + pg0 + (i + lane) * CA_WARPS];
+          if (ids < 0 || ids >= p.c.pool_pages) {
+            set_status(p.c.status, SDV_ERR_PAGE_RANGE);
+            ids = 0;  // some page of the pool: the call's outputs hold nothing meaningful
+          }
+        }
+      }
+      return __shfl_sync(0xffffffffu, ids, i & 31);
+    };
+    if (mine > 0) load_page(nxt, p.c, page_id(0), h, g, t);
+    for (int i = 0; i < mine; ++i) {
+      cur = nxt;
+      if (i + 1 < mine) load_page(nxt, p.c, page_id(i + 1), h, g, t);
+      const int key0 = (pg0 + i * CA_WARPS) * kPage;
+      float s[2][4];
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+#pragma unroll
+        for (int ks = 0; ks < F::KSTEPS; ++ks) {
+          if constexpr (F::kCodes) {
+            const uint32_t w = cur.k[n][ks];
+            mma_f16(s[n], qf[ks], e4m3x2_to_f16x2(w & 0xFFFFu), e4m3x2_to_f16x2(w >> 16));
+          } else {
+            mma_bf16(s[n], qf[ks], cur.k[n][2 * ks], cur.k[n][2 * ks + 1]);
+          }
+        }
+      }
+      // base-2 logits; s[n][2 r + c] is row g + 8 r, key key0 + 8 n + 2 t + c
+      float vs[2][2];
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int cc = 0; cc < 2; ++cc) {
+          float ksc = 1.f;
+          vs[n][cc] = 1.f;
+          if constexpr (F::kCodes) {
+            ksc = scale_value(cur.sc[n] >> (8 * cc));
+            vs[n][cc] = scale_value((cur.sc[n] >> (16 + 8 * cc)) + kSplitBias);
+          }
+          s[n][cc] *= cz[0] * ksc;
+          s[n][2 + cc] *= cz[1] * ksc;
+        }
+      const bool full = key0 + kPage - 1 <= pmin && (window <= 0 || key0 > pmax - window);
+      if (!full) {
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int key = key0 + 8 * n + 2 * t + (x & 1), ps = pos[x >> 1];
+            if (key > ps || (window > 0 && key <= ps - window)) s[n][x] = -INFINITY;
+          }
+        // keys that no row of the item sees may hold anything: their weight is
+        // 0 and their values are taken as 0
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int key = key0 + 2 * t + (r & 1) + 8 * (r >> 1);
+          if (key > pmax || (window > 0 && key <= pmin - window)) {
+            vs[r >> 1][r & 1] = 0.f;
+#pragma unroll
+            for (int w = 0; w < F::VW; ++w) cur.v[r][w] = 0u;
+          }
+        }
+      }
+      float top[2];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) top[r] = fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]), fmaxf(s[1][2 * r], s[1][2 * r + 1]));
+      if (__any_sync(0xffffffffu, top[0] > m[0] || top[1] > m[1])) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          float x = fmaxf(top[r], m[r]);
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+          const float a = fast_ex2(m[r] - x);
+          m[r] = x;
+          l[r] *= a;
+#pragma unroll
+          for (int j = 0; j < F::NT; ++j) o[j][2 * r] *= a, o[j][2 * r + 1] *= a;
+        }
+      }
+      uint32_t pa[4];
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const float x = fast_ex2(s[n][2 * r] - m[r]), y = fast_ex2(s[n][2 * r + 1] - m[r]);
+          l[r] += x + y;
+          if constexpr (F::kCodes) {
+            const __half2 w = __floats2half2_rn(x * vs[n][0], y * vs[n][1]);
+            pa[2 * n + r] = *reinterpret_cast<const uint32_t*>(&w);
+          } else {
+            pa[2 * n + r] = pack_bf16x2(x, y);
+          }
+        }
+#pragma unroll
+      for (int w = 0; w < F::VW; ++w) {
+        if constexpr (F::kCodes) {
+          const uint32_t a0 = __byte_perm(cur.v[0][w], cur.v[1][w], 0x5140), a1 = __byte_perm(cur.v[0][w], cur.v[1][w], 0x7362);
+          const uint32_t b0 = __byte_perm(cur.v[2][w], cur.v[3][w], 0x5140), b1 = __byte_perm(cur.v[2][w], cur.v[3][w], 0x7362);
+          mma_f16(o[4 * w], pa, e4m3x2_to_f16x2(a0 & 0xFFFFu), e4m3x2_to_f16x2(b0 & 0xFFFFu));
+          mma_f16(o[4 * w + 1], pa, e4m3x2_to_f16x2(a0 >> 16), e4m3x2_to_f16x2(b0 >> 16));
+          mma_f16(o[4 * w + 2], pa, e4m3x2_to_f16x2(a1 & 0xFFFFu), e4m3x2_to_f16x2(b1 & 0xFFFFu));
+          mma_f16(o[4 * w + 3], pa, e4m3x2_to_f16x2(a1 >> 16), e4m3x2_to_f16x2(b1 >> 16));
+        } else {
+          mma_bf16(o[2 * w], pa, __byte_perm(cur.v[0][w], cur.v[1][w], 0x5410), __byte_perm(cur.v[2][w], cur.v[3][w], 0x5410));
+          mma_bf16(o[2 * w + 1], pa, __byte_perm(cur.v[0][w], cur.v[1][w], 0x7632), __byte_perm(cur.v[2][w], cur.v[3][w], 0x7632));
+        }
+      }
+    }
+
+    // the warps' parts into shared memory, then joined: 8 threads a row
+    const float undo = F::kCodes ? 1.f / (1 << kSplitBias) : 1.f;
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+      if (t == 0) {
+        s_ml[warp * 2 * ROWS + g + 8 * r] = m[r];
+        s_ml[warp * 2 * ROWS + ROWS + g + 8 * r] = l[r];
+      }
+#pragma unroll
+      for (int j = 0; j < F::NT; ++j) {
+        s_o[(warp * ROWS + g + 8 * r) * D + out_col<D, FMT>(2 * t, j)] = o[j][2 * r] * undo;
+        s_o[(warp * ROWS + g + 8 * r) * D + out_col<D, FMT>(2 * t + 1, j)] = o[j][2 * r + 1] * undo;
+      }
+    }
+    __syncthreads();
+    constexpr int PER = D / 8;
+    const int row = tid >> 3, c0 = (tid & 7) * PER;
+    float acc[PER], M = kNoMax, L = 0.f;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) acc[j] = 0.f;
+#pragma unroll
+    for (int w = 0; w < CA_WARPS; ++w) M = fmaxf(M, s_ml[w * 2 * ROWS + row]);
+#pragma unroll
+    for (int w = 0; w < CA_WARPS; ++w) {
+      const float a = fast_ex2(s_ml[w * 2 * ROWS + row] - M);
+      L += a * s_ml[w * 2 * ROWS + ROWS + row];
+#pragma unroll
+      for (int j = 0; j < PER; ++j) acc[j] += a * s_o[(w * ROWS + row) * D + c0 + j];
+    }
+    // the blocks that hold pages of this item
+    const long long u0 = s_base[b] + item * n_pages;
+    const int c_first = static_cast<int>(u0 / per_cta), c_last = static_cast<int>((u0 + n_pages - 1) / per_cta);
+    bool write = row < n_rows && !dead;
+    if (c_first != c_last) {
+      // a block has at most two cut items: one begun before its run (slot 0)
+      // and one that goes on behind it (slot 1)
+      constexpr int PF = part_floats(D);
+      float* mine_part = p.part + (2LL * blockIdx.x + (c_first == (int)blockIdx.x)) * PF;
+#pragma unroll
+      for (int j = 0; j < PER; j += 4)
+        *reinterpret_cast<float4*>(mine_part + row * D + c0 + j) = make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
+      if ((tid & 7) == 0) {
+        mine_part[ROWS * D + row] = M;
+        mine_part[ROWS * D + ROWS + row] = L;
+      }
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) {
+        s_last = atomicAdd(p.counters + c_first, 1) == c_last - c_first;
+        if (s_last) p.counters[c_first] = 0;
+        __threadfence();
+      }
+      __syncthreads();
+      write = write && s_last;
+      if (s_last) {
+        M = kNoMax;
+        for (int cta = c_first; cta <= c_last; ++cta)
+          M = fmaxf(M, __ldcg(p.part + (2LL * cta + (cta == c_first)) * PF + ROWS * D + row));
+        L = 0.f;
+#pragma unroll
+        for (int j = 0; j < PER; ++j) acc[j] = 0.f;
+        for (int cta = c_first; cta <= c_last; ++cta) {
+          const float* src = p.part + (2LL * cta + (cta == c_first)) * PF;
+          const float a = fast_ex2(__ldcg(src + ROWS * D + row) - M);
+          L += a * __ldcg(src + ROWS * D + ROWS + row);
+#pragma unroll
+          for (int j = 0; j < PER; j += 4) {
+            const float4 x = __ldcg(reinterpret_cast<const float4*>(src + row * D + c0 + j));
+            acc[j] += a * x.x, acc[j + 1] += a * x.y, acc[j + 2] += a * x.z, acc[j + 3] += a * x.w;
+          }
+        }
+      }
+    }
+    if (write) {
+      const float inv = L == 0.f ? 0.f : 1.f / L;  // a row that sees nothing gives 0
+      const int rr = row0 + row;
+      __nv_bfloat16* dst = p.out + (long long)(sq.off + rr / group) * p.out_stride + (long long)(h * group + rr % group) * D + c0;
+#pragma unroll
+      for (int j = 0; j < PER; j += 8)
+        *reinterpret_cast<uint4*>(dst + j) =
+            make_uint4(pack_bf16x2(acc[j] * inv, acc[j + 1] * inv), pack_bf16x2(acc[j + 2] * inv, acc[j + 3] * inv),
+                       pack_bf16x2(acc[j + 4] * inv, acc[j + 5] * inv), pack_bf16x2(acc[j + 6] * inv, acc[j + 7] * inv));
+    }
+    __syncthreads();
+    u += n_here;
+  }
+}
+
+size_t smem_bytes(int D, int B) {
+  return (CA_WARPS * ROWS * D + CA_WARPS * 2 * ROWS) * sizeof(float) + (B + 1) * sizeof(long long) + (2 * B + 1) * sizeof(int);
+}
+
+template <int D, int FMT>
+cudaError_t launch_one(const ChunkAttnParams& p, int grid, cudaStream_t stream) {
+  return launch_pdl(chunk_attn_kernel<D, FMT>, dim3(grid), dim3(CA_THREADS), smem_bytes(D, p.c.B), stream, p);
+}
+
+template <int D, int FMT>
+cudaError_t setup_one() {
+  return cudaFuncSetAttribute(chunk_attn_kernel<D, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              static_cast<int>(smem_bytes(D, kMaxChunkSlots)));
+}
+
+}  // namespace
+
+cudaError_t setup_chunk_attn(int head_dim, int cache_format) {
+  if (head_dim == 64)
+    return cache_format == SDV_CACHE_BF16 ? setup_one<64, SDV_CACHE_BF16>() : setup_one<64, SDV_CACHE_E4M3>();
+  return cache_format == SDV_CACHE_BF16 ? setup_one<128, SDV_CACHE_BF16>() : setup_one<128, SDV_CACHE_E4M3>();
+}
+
+int chunk_attn_grid(int, int, int sms) { return 2 * sms; }
+
+cudaError_t launch_chunk_attn(int head_dim, int cache_format, const ChunkAttnParams& p, int grid, cudaStream_t stream) {
+  if (head_dim == 64)
+    return cache_format == SDV_CACHE_BF16 ? launch_one<64, SDV_CACHE_BF16>(p, grid, stream)
+                                          : launch_one<64, SDV_CACHE_E4M3>(p, grid, stream);
+  return cache_format == SDV_CACHE_BF16 ? launch_one<128, SDV_CACHE_BF16>(p, grid, stream)
+                                        : launch_one<128, SDV_CACHE_E4M3>(p, grid, stream);
+}
+
+}  // namespace sdv

@@ -305,6 +305,9 @@ struct AdmitParams {
 // Append admitted sequences to a slot table (one block).
 cudaError_t launch_admit(const AdmitParams& p, cudaStream_t stream);
 
+// SDV_ERR_CUDA, with the error kept for sdv_last_cuda_error
+sdv_status cuda_fail(cudaError_t e);
+
 // count of kernels launched by this library
 void note_launch(int n = 1);
 
