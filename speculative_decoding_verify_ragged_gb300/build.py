@@ -20,7 +20,7 @@ LIB = os.path.join(HERE, "libsdv.so")
 BUILD_TRACE = os.path.join(HERE, "_build_trace")
 LIB_TRACE = os.path.join(HERE, "libsdv_trace.so")
 SOURCES = ("api.cu", "gemm.cu", "gemm_tc.cu", "gemm_tc_q4.cu", "gemm_q4.cu", "attention.cu", "attention_tc.cu", "cache_api.cu", "cache_io.cu",
-           "chunk_attention.cu", "step_kernels.cu", "noalloc.cu", "sched.cpp", "ngram.cpp")
+           "chunk_attention.cu", "chunk_attention_tc.cu", "step_kernels.cu", "noalloc.cu", "sched.cpp", "ngram.cpp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -205,12 +205,12 @@ static bool encode_f16_2d(CUtensorMap* m, const void* base, uint64_t rows, uint6
 }
 
 // KV pool [pages, n_kv, 2, page, D] as a 5-D tensor; box = 64 of D x 16 slots.
-static bool encode_kv(CUtensorMap* m, const void* base, const sdv_config& c, int pool_pages) {
+bool encode_kv_map(CUtensorMap* m, const void* base, int n_kv, int head_dim, int pool_pages) {
   auto fn = encode_fn();
   if (!fn) return false;
-  const uint64_t D = c.head_dim, P = c.page_size;
-  cuuint64_t dims[5] = {D, P, 2, static_cast<cuuint64_t>(c.n_kv), static_cast<cuuint64_t>(pool_pages)};
-  cuuint64_t strides[4] = {D * 2, P * D * 2, 2 * P * D * 2, static_cast<cuuint64_t>(c.n_kv) * 2 * P * D * 2};
+  const uint64_t D = head_dim, P = 16;
+  cuuint64_t dims[5] = {D, P, 2, static_cast<cuuint64_t>(n_kv), static_cast<cuuint64_t>(pool_pages)};
+  cuuint64_t strides[4] = {D * 2, P * D * 2, 2 * P * D * 2, static_cast<cuuint64_t>(n_kv) * 2 * P * D * 2};
   cuuint32_t box[5] = {64, 16, 1, 1, 1};
   cuuint32_t es[5] = {1, 1, 1, 1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(base), dims, strides, box, es,
@@ -561,7 +561,7 @@ static int attn_min_chunk(const AttnPlan& plan) { return plan.tc ? 32 : 8; }
 static sdv_status run_attention(sdv_ctx* c, const sdv_batch* b, const float* q, __nv_bfloat16* out,
                                 long long out_lo_off, int* status, cudaStream_t s) {
   CUtensorMap kv;
-  if (!encode_kv(&kv, b->kv_pool, c->cfg, b->num_pool_pages)) return SDV_ERR_CUDA;
+  if (!encode_kv_map(&kv, b->kv_pool, c->cfg.n_kv, c->cfg.head_dim, b->num_pool_pages)) return SDV_ERR_CUDA;
   AttnParams a;
   a.q = q;
   a.out = out;

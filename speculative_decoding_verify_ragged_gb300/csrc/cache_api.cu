@@ -1,6 +1,7 @@
 // C ABI of the paged cache's operators (include/sdv_cache.h): argument checks,
 // the handle and the launches.
 #include <cmath>
+#include <cstring>
 #include <new>
 
 #include "chunk.cuh"
@@ -8,8 +9,8 @@
 struct sdv_cache {
   sdv_cache_config cfg;
   int device, sms, max_rows, max_slots, grid;
-  float* part;
-  int* counters;
+  float *part, *part_tc;
+  int *counters, *counters_tc;
   sdv::RopeTurns turns;
 };
 
@@ -31,16 +32,22 @@ int sms_of(int dev) {
   return cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess ? n : 0;
 }
 
+// Packed rows (tokens times heads of a group) of a sequence up to which the
+// mma.sync kernel takes it: one of its 16-row items.
+constexpr int kSmallRows = 16;
+
 struct Space {
-  size_t counters, part, total;
+  size_t counters, counters_tc, part, part_tc, total;
   int grid;
 };
 Space space(const sdv_cache_config& c, int sms) {
   Space s{};
   s.grid = chunk_attn_grid(c.head_dim, c.cache_format, sms);
   s.counters = 0;
-  s.part = up256(s.grid * sizeof(int));
-  s.total = s.part + up256(static_cast<size_t>(2) * s.grid * 16 * (c.head_dim + 2) * sizeof(float));
+  s.counters_tc = up256(s.grid * sizeof(int));
+  s.part = s.counters_tc + up256(2 * sms * sizeof(int));
+  s.part_tc = s.part + up256(static_cast<size_t>(2) * s.grid * 16 * (c.head_dim + 2) * sizeof(float));
+  s.total = s.part_tc + up256(chunk_attn_tc_part_floats(c.head_dim, sms) * sizeof(float));
   return s;
 }
 
@@ -109,6 +116,7 @@ extern "C" sdv_status sdv_cache_create(const sdv_cache_config* cfg, void* worksp
   const Space s = space(*cfg, sms);
   if (workspace_bytes < s.total) return SDV_ERR_CAPACITY;
   e = setup_chunk_attn(cfg->head_dim, cfg->cache_format);
+  if (e == cudaSuccess) e = setup_chunk_attn_tc(cfg->head_dim, cfg->cache_format);
   if (e != cudaSuccess) return cuda_fail(e);
   sdv_cache* h = new (std::nothrow) sdv_cache;
   if (!h) return SDV_ERR_INTERNAL;
@@ -119,7 +127,9 @@ extern "C" sdv_status sdv_cache_create(const sdv_cache_config* cfg, void* worksp
   h->max_slots = max_slots;
   h->grid = s.grid;
   h->counters = reinterpret_cast<int*>(static_cast<uint8_t*>(workspace) + s.counters);
+  h->counters_tc = reinterpret_cast<int*>(static_cast<uint8_t*>(workspace) + s.counters_tc);
   h->part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + s.part);
+  h->part_tc = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + s.part_tc);
   for (int j = 0; j < 64; ++j) {
     h->turns.f[j] = 0;
     if (cfg->rope_theta > 0.f && j < cfg->head_dim / 2) {
@@ -128,7 +138,7 @@ extern "C" sdv_status sdv_cache_create(const sdv_cache_config* cfg, void* worksp
       h->turns.f[j] = static_cast<unsigned long long>(std::ldexp(turn, 64));
     }
   }
-  e = cudaMemsetAsync(h->counters, 0, s.grid * sizeof(int), static_cast<cudaStream_t>(stream));
+  e = cudaMemsetAsync(h->counters, 0, s.part, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) {
     delete h;
     return cuda_fail(e);
@@ -181,9 +191,24 @@ extern "C" sdv_status sdv_cache_attention(sdv_cache* h, const sdv_chunk* chunk, 
   p.out = static_cast<__nv_bfloat16*>(out);
   p.q_stride = q_stride;
   p.out_stride = out_stride;
+  p.scale_log2 = kLog2e / std::sqrt(static_cast<float>(d));
+  p.small_rows = 0x7FFFFFFF;
+  const int group = h->cfg.n_q / h->cfg.n_kv;
+  if ((long long)(chunk->max_q < chunk->T ? chunk->max_q : chunk->T) * group > kSmallRows) {
+    p.small_rows = kSmallRows;
+    p.part = h->part_tc;
+    p.counters = h->counters_tc;
+    CUtensorMap map;
+    if (h->cfg.cache_format == SDV_CACHE_BF16) {
+      if (!encode_kv_map(&map, chunk->kv_pool, h->cfg.n_kv, d, chunk->num_pool_pages)) return SDV_ERR_CUDA;
+    } else {
+      std::memset(&map, 0, sizeof(map));  // the codes are not loaded through it
+    }
+    const cudaError_t e = launch_chunk_attn_tc(d, h->cfg.cache_format, map, p, h->sms, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e);
+  }
   p.part = h->part;
   p.counters = h->counters;
-  p.scale_log2 = kLog2e / std::sqrt(static_cast<float>(d));
   return launched(launch_chunk_attn(d, h->cfg.cache_format, p, h->grid, static_cast<cudaStream_t>(stream)));
 }
 

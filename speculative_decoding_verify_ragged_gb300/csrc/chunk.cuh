@@ -120,10 +120,16 @@ struct ChunkAttnParams {
   const __nv_bfloat16* q = nullptr;
   __nv_bfloat16* out = nullptr;
   long long q_stride = 0, out_stride = 0;
-  float* part = nullptr;     // [2 * grid][16 * (D + 2)] partial results of cut items
-  int* counters = nullptr;   // [grid] arrivals, zero between launches
+  float* part = nullptr;     // partial results of cut items, two per block of the launch
+  int* counters = nullptr;   // arrivals at them, zero between launches
+  int small_rows = 0;        // packed rows up to which a sequence is the mma.sync kernel's
   float scale_log2 = 0.f;    // log2(e) / sqrt(head_dim)
 };
+// Sequences of many rows on tcgen05, one block per SM (chunk_attention_tc.cu).
+size_t chunk_attn_tc_part_floats(int head_dim, int grid);
+cudaError_t setup_chunk_attn_tc(int head_dim, int cache_format);
+cudaError_t launch_chunk_attn_tc(int head_dim, int cache_format, const CUtensorMap& map, const ChunkAttnParams& p, int grid,
+                                 cudaStream_t stream);
 // Blocks a launch of the mma.sync kernel uses at most (its partials and counters are sized by it).
 int chunk_attn_grid(int head_dim, int cache_format, int sms);
 // Once per device before the first launch.

@@ -121,6 +121,11 @@ __global__ void __launch_bounds__(CA_THREADS, 2) chunk_attn_kernel(const ChunkAt
   if (!load_chunk(p.c, s_off, s_len)) return;
 
   // pages of each of a sequence's items (those that any of its rows sees), first page
+  auto seq_of = [&](int b) {
+    SeqRows s = seq_rows(s_off, s_len, b);
+    if (s.n * group > p.small_rows) s.n = 0;  // the tcgen05 kernel's
+    return s;
+  };
   auto seq_pages = [&](const SeqRows& s, int& lo) {
     lo = window > 0 ? max(0, s.pos0 - window + 1) / kPage : 0;
     return s.n > 0 ? max(1, (s.len + kPage - 1) / kPage - lo) : 0;
@@ -130,7 +135,7 @@ __global__ void __launch_bounds__(CA_THREADS, 2) chunk_attn_kernel(const ChunkAt
     const int per = (B + CA_THREADS - 1) / CA_THREADS, b0 = min(B, tid * per), b1 = min(B, b0 + per);
     long long sum = 0;
     for (int b = b0; b < b1; ++b) {
-      const SeqRows s = seq_rows(s_off, s_len, b);
+      const SeqRows s = seq_of(b);
       int lo;
       const int u = seq_pages(s, lo);
       s_base[b] = sum;
@@ -165,7 +170,7 @@ __global__ void __launch_bounds__(CA_THREADS, 2) chunk_attn_kernel(const ChunkAt
       }
       b = lo;
     }
-    const SeqRows sq = seq_rows(s_off, s_len, b);
+    const SeqRows sq = seq_of(b);
     int lo_page;
     const int n_pages = seq_pages(sq, lo_page), tiles = seq_tiles(sq);
     const long long item = (u - s_base[b]) / n_pages;  // within the sequence: key head, then tile

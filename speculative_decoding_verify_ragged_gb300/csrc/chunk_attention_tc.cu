@@ -1,0 +1,865 @@
+// Attention of a ragged chunk over the paged cache on the 5th-generation tensor
+// cores, for sequences whose rows fill a 128-row tile (prompts, pieces of them).
+//
+// An item is two tiles of 128 packed query rows (row = token, head of the group)
+// of one (sequence, key head) against the blocks of 128 keys that they see.  The
+// items' blocks are laid end to end and cut into equal runs, one per SM; an item
+// cut between SMs is joined, in SM order, by the last to arrive.  Per block
+//   S_t = Q_t K^T  (M = 128 rows, N = 128 keys),  O_t += P_t V  (P_t from TMEM)
+// run for tile 0 and tile 1 in turn, so the tensor cores work on one tile while
+// the other's softmax runs: one thread holds one row, reads its scores from
+// TMEM once and writes the weights over them in 16 bits.  The maximum is a
+// bound that moves only when a row's scores pass it by 2^8 (then the block is taken again and O is
+// rescaled in TMEM), so a block is one pass.
+//
+// TMEM: S_0, S_1 (128 columns each; P_t over S_t's first 64), O_0, O_1 (D each).
+// Shared memory: Q tiles and a ring of K and V blocks, rows of 128 bytes,
+// 128-byte swizzle.  A bf16 cache is loaded by TMA, a page's 64-wide half a copy; e4m3
+// codes go through registers (four warps) and land as fp16, scales applied, exact.
+// Values of keys that a block's rows cannot see are zeroed in shared memory, so
+// that nothing behind a sequence's end is ever multiplied.
+#include "chunk.cuh"
+#include "tcgen05.cuh"
+
+namespace sdv {
+namespace {
+
+using namespace tc;
+
+constexpr int BM = 128;              // query rows of a tile
+constexpr int BK = 128;              // keys of a block
+constexpr int BPAGES = BK / kPage;
+constexpr int HALF = BM * 128;       // 64 columns of 128 rows: 16 KB
+constexpr float kNoMax = -1e30f;     // the bound before the first visible key, in base-2 logits
+constexpr float kSlack = 8.f;        // log2 of what a weight may reach before its bound moves
+
+constexpr int MMA_WARP = 8, TMA_WARP = 9, CONV_WARP = 12;
+
+template <int D, int FMT>
+struct Cfg {
+  static constexpr bool kCodes = FMT == SDV_CACHE_E4M3;
+  static constexpr int THREADS = kCodes ? 512 : 384;
+  static constexpr int HALVES = D / 64;
+  static constexpr int SLOT = HALVES * HALF;          // K or V of one block
+  static constexpr int NS = D == 128 ? 5 : 8;
+  static constexpr int OFF_Q = NS * SLOT;
+  static constexpr int OFF_BAR = OFF_Q + 2 * SLOT;
+  static constexpr int NBAR = 2 * NS + 2 * 4 + 2;     // full, empty; s, p, q, o of each tile; tail, done
+  static constexpr int SMEM = 1024 + OFF_BAR + NBAR * 8 + 64;
+  static_assert(SMEM <= 227 * 1024, "shared memory");
+  static constexpr int FULL_COUNT = kCodes ? 4 : 1;
+  // registers a thread: softmax, products and copies, conversion (launched with
+  // 65536 / THREADS, rounded down to a multiple of 8: 168, or 128)
+  static constexpr int R_SOFT = kCodes ? 168 : 192, R_ISSUE = kCodes ? 72 : 120, R_CONV = 104;
+  static_assert(2 * R_SOFT + R_ISSUE + (kCodes ? R_CONV : 0) <= (kCodes ? 4 * 128 : 3 * 168), "register shares");
+  static constexpr int T_O = 2 * BK;                  // TMEM columns of O_0
+};
+
+__device__ __forceinline__ uint64_t desc_mn(uint32_t saddr) {  // V rows read MN-major: 16 KB between 64-column halves
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
+  d |= static_cast<uint64_t>(HALF >> 4) << 16;
+  d |= static_cast<uint64_t>(1024 >> 4) << 32;
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(2) << 61;
+  return d;
+}
+
+// fp32 accumulate; bf16 operands, or fp16 (format 0)
+__host__ __device__ constexpr uint32_t idesc(bool f16, int N, bool b_mn) {
+  return (1u << 4) | (f16 ? 0u : (1u << 7) | (1u << 10)) | (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(N >> 3) << 17) |
+         (static_cast<uint32_t>(BM >> 4) << 24);
+}
+
+__device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t id, uint32_t acc) {
+  asm volatile(
+      "{\n"
+      " .reg .pred p;\n"
+      " setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n"
+      "}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b), "r"(id), "r"(acc));
+}
+
+// Registers per thread of this warpgroup (the shares of all add up to the launch's).
+template <int N>
+__device__ __forceinline__ void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+#define R8(v, o) "=r"(v[o]), "=r"(v[o + 1]), "=r"(v[o + 2]), "=r"(v[o + 3]), "=r"(v[o + 4]), "=r"(v[o + 5]), "=r"(v[o + 6]), "=r"(v[o + 7])
+#define W8(v, o) "+r"(v[o]), "+r"(v[o + 1]), "+r"(v[o + 2]), "+r"(v[o + 3]), "+r"(v[o + 4]), "+r"(v[o + 5]), "+r"(v[o + 6]), "+r"(v[o + 7])
+#define I8(v, o) "r"(v[o]), "r"(v[o + 1]), "r"(v[o + 2]), "r"(v[o + 3]), "r"(v[o + 4]), "r"(v[o + 5]), "r"(v[o + 6]), "r"(v[o + 7])
+
+// 32 lanes x 32 columns; the registers hold the values only after tmem_wait_ld.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, "
+      "%18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : R8(r, 0), R8(r, 8), R8(r, 16), R8(r, 24)
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : W8(r, 0), W8(r, 8), W8(r, 16), W8(r, 24)::"memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, "
+      "%18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+      I8(r, 0), I8(r, 8), I8(r, 16), I8(r, 24)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Two fp32 lanes in one instruction.
+__device__ __forceinline__ uint64_t f2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unf2(uint64_t v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// The blocks of 256 packed rows of a sequence, and what each of its tiles sees.
+struct Item {
+  int row0, rows;       // packed rows
+  int klo, khi;         // keys that a row sees (khi = 0: none)
+  int page_lo, blocks;  // first page; blocks of BK keys (one at least)
+};
+__device__ __forceinline__ Item make_item(const SeqRows& s, int group, int window, int qt) {
+  Item it;
+  it.row0 = qt * 2 * BM;
+  it.rows = min(2 * BM, s.n * group - it.row0);
+  const int pmin = s.pos0 + it.row0 / group, pmax = s.pos0 + (it.row0 + it.rows - 1) / group;
+  it.khi = max(0, pmax + 1);
+  it.klo = min(it.khi, window > 0 ? max(0, pmin - window + 1) : 0);
+  it.page_lo = it.klo / kPage;
+  it.blocks = max(1, (it.khi - it.page_lo * kPage + BK - 1) / BK);
+  return it;
+}
+// The item's blocks [b0, b1) that tile t needs, and its rows' range of positions.
+struct Tile {
+  int rows, pmin, pmax, b0, b1;
+};
+__device__ __forceinline__ Tile make_tile(const SeqRows& s, const Item& it, int group, int window, int t) {
+  Tile x;
+  x.rows = min(BM, it.rows - t * BM);
+  x.b0 = x.b1 = 0;
+  x.pmin = x.pmax = -1;
+  if (x.rows <= 0) return x;
+  const int r0 = it.row0 + t * BM;
+  x.pmin = s.pos0 + r0 / group;
+  x.pmax = s.pos0 + (r0 + x.rows - 1) / group;
+  const int hi = x.pmax + 1, lo = window > 0 ? max(0, x.pmin - window + 1) : 0;
+  if (hi <= lo || hi <= 0) return x;
+  x.b0 = (lo - it.page_lo * kPage) / BK;
+  x.b1 = (hi - it.page_lo * kPage + BK - 1) / BK;
+  return x;
+}
+
+// A place in the walk over all items' blocks: sequence, key head, item, block.
+struct Place {
+  int b, h, qt, blk;
+};
+
+template <int D, int FMT>
+__global__ void __launch_bounds__(Cfg<D, FMT>::THREADS, 1)
+    chunk_attn_tc_kernel(const __grid_constant__ CUtensorMap tmKV, const ChunkAttnParams p) {
+  using C = Cfg<D, FMT>;
+  extern __shared__ uint8_t smem_raw[];
+  griddep_launch_dependents();
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+  uint64_t* empty = full + C::NS;
+  uint64_t* s_full = empty + C::NS;  // [2] scores of tile t are in TMEM
+  uint64_t* p_full = s_full + 2;     // [2] its weights are, and O_t may be added to
+  uint64_t* q_full = p_full + 2;     // [2]
+  uint64_t* o_full = q_full + 2;     // [2] the item's last product of tile t is in O_t
+  uint64_t* tail = o_full + 2;       // copies of a block whose end is zeroed before use
+  uint64_t* done = tail + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+  __shared__ long long s_scan[2];        // first unit of the sequence the run starts in; units of the launch
+  __shared__ Place s_start;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int i = 0; i < C::NS; ++i) {
+      mbar_init(&full[i], C::FULL_COUNT);
+      mbar_init(&empty[i], 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&s_full[t], 1);
+      mbar_init(&p_full[t], 4);
+      mbar_init(&q_full[t], 4);
+      mbar_init(&o_full[t], 1);
+    }
+    mbar_init(tail, 1);
+    mbar_init(done, 1);
+    fence_barrier_init();
+  }
+  if (warp == MMA_WARP) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tmem_slot)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  griddep_wait();
+
+  const int B = p.c.B, group = p.c.n_q / p.c.n_kv, window = p.c.window, n_kv = p.c.n_kv;
+  auto seq_of = [&](int b) {
+    const int o = p.c.row_offsets[b], e = p.c.row_offsets[b + 1], len = p.c.kv_lens[b];
+    SeqRows s{o, e - o, len, len - (e - o)};
+    if (s.n * group <= p.small_rows) s.n = 0;  // the other kernel's
+    return s;
+  };
+  auto items_of = [&](const SeqRows& s) { return (int)(((long long)s.n * group + 2 * BM - 1) / (2 * BM)); };
+
+  // ---- the chunk's check and this block's run of units ----
+  const int status0 = read_status(p.c.status);
+  const bool dead0 = __syncthreads_or(status0 != 0);  // one verdict for the block
+  bool good;
+  {
+    int bad = 0;
+    for (int b = tid; b < B; b += blockDim.x) {
+      const int o = p.c.row_offsets[b], e = p.c.row_offsets[b + 1], len = p.c.kv_lens[b];
+      if (o < 0 || e < o || e > p.c.T || e - o > p.c.max_q || (b == 0 && o != 0) || len < 0) bad |= 1;
+      if (len > (long long)p.c.max_pages * kPage) bad |= 2;
+    }
+    const bool b1 = __syncthreads_or(bad & 1), b2 = __syncthreads_or(bad & 2);
+    if ((b1 || b2) && tid == 0) set_status(p.c.status, b1 ? SDV_ERR_BAD_INPUT : SDV_ERR_PAGE_RANGE);
+    good = !b1 && !b2;
+  }
+  long long u_begin = 0, u_end = 0, per_cta = 1;
+  if (good) {
+    // blocks of one key head of each sequence, a warp a sequence, into the ring (not in use yet)
+    int* s_units = reinterpret_cast<int*>(smem);                                                 // [B]
+    for (int b = warp; b < B; b += blockDim.x / kWarp) {
+      const SeqRows s = seq_of(b);
+      int sum = 0;
+      for (int qt = lane; qt < items_of(s); qt += kWarp) sum += make_item(s, group, window, qt).blocks;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      if (lane == 0) s_units[b] = sum;
+    }
+    __syncthreads();
+    if (warp == 0) {
+      // total, then the sequence, key head, item and block of the run's first unit
+      long long total = 0;
+      for (int b0 = 0; b0 < B; b0 += kWarp) {
+        long long v = b0 + lane < B ? (long long)s_units[b0 + lane] * n_kv : 0;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        total += v;
+      }
+      const long long per = max(1LL, (total + gridDim.x - 1) / gridDim.x), u = (long long)blockIdx.x * per;
+      if (u < total) {
+        long long base = 0;
+        int b = -1;
+        for (int b0 = 0; b0 < B && b < 0; b0 += kWarp) {
+          const long long v = b0 + lane < B ? (long long)s_units[b0 + lane] * n_kv : 0;
+          long long inc = v;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const long long w = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += w;
+          }
+          const unsigned hit = __ballot_sync(0xffffffffu, base + inc > u);
+          if (hit) {
+            const int l = __ffs(hit) - 1;
+            b = b0 + l;
+            base += __shfl_sync(0xffffffffu, inc - v, l);
+          } else {
+            base += __shfl_sync(0xffffffffu, inc, 31);
+          }
+        }
+        const SeqRows s = seq_of(b);
+        const int per_head = s_units[b], h = static_cast<int>((u - base) / per_head);
+        int rest = static_cast<int>((u - base) - (long long)h * per_head), qt = -1;
+        for (int q0 = 0; qt < 0; q0 += kWarp) {
+          const int v = q0 + lane < items_of(s) ? make_item(s, group, window, q0 + lane).blocks : 0;
+          int inc = v;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int w = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += w;
+          }
+          const unsigned hit = __ballot_sync(0xffffffffu, inc > rest);
+          if (hit) {
+            const int l = __ffs(hit) - 1;
+            qt = q0 + l;
+            rest -= __shfl_sync(0xffffffffu, inc - v, l);
+          } else {
+            rest -= __shfl_sync(0xffffffffu, inc, 31);
+          }
+        }
+        if (lane == 0) s_start = Place{b, h, qt, rest};
+      }
+      if (lane == 0) {
+        s_scan[0] = per;
+        s_scan[1] = total;
+      }
+    }
+    fence_proxy_async_smem();  // the ring's next writers are copies
+    __syncthreads();
+    per_cta = s_scan[0];
+    u_begin = (long long)blockIdx.x * per_cta;
+    u_end = min(s_scan[1], u_begin + per_cta);
+  }
+  // calls f(sequence, key head, item, its first unit, blocks [b0, b1) of this run) for each part of the run
+  auto walk = [&](auto&& f) {
+    if (u_begin >= u_end) return;
+    Place at = s_start;
+    SeqRows s = seq_of(at.b);
+    for (long long u = u_begin;;) {
+      const Item it = make_item(s, group, window, at.qt);
+      const int n = static_cast<int>(min((long long)(it.blocks - at.blk), u_end - u));
+      if (!f(s, at.b, at.h, it, u - at.blk, at.blk, at.blk + n)) return;
+      u += n;
+      if (u >= u_end) return;
+      at.blk = 0;
+      if (++at.qt == items_of(s)) {
+        at.qt = 0;
+        if (++at.h == n_kv) {
+          at.h = 0;
+          do s = seq_of(++at.b);
+          while (s.n == 0);
+        }
+      }
+    }
+  };
+  auto clip = [](Tile x, int b0, int b1) {  // the tile's blocks within [b0, b1)
+    x.b0 = max(x.b0, b0);
+    x.b1 = min(x.b1, b1);
+    if (x.b0 >= x.b1) x.b0 = x.b1 = 0;
+    return x;
+  };
+
+  auto load = [&]() {
+    // ---------------- loads: K and V of each block into the ring, in turn ----------------
+    {
+      int slot = 0;
+      uint32_t phase = 0, tail_phase = 0;
+      bool dead = dead0;
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (!dead && !mbar_wait(bar, parity)) {
+          set_status(p.c.status, SDV_ERR_TIMEOUT);
+          dead = true;
+        }
+        dead = __any_sync(0xffffffffu, dead);
+      };
+      walk([&](const SeqRows& s, int b, int h, const Item& it, long long, int b0, int b1) {
+        const Tile t0 = clip(make_tile(s, it, group, window, 0), b0, b1), t1 = clip(make_tile(s, it, group, window, 1), b0, b1);
+        const int* table = p.c.page_table + (long long)b * p.c.max_pages;
+        for (int j = b0; j < b1; ++j) {
+          if (!((j >= t0.b0 && j < t0.b1) || (j >= t1.b0 && j < t1.b1))) continue;
+          const int key0 = it.page_lo * kPage + j * BK;
+          const int vlo = max(0, it.klo - key0), vhi = min(BK, it.khi - key0);  // the block's rows that are seen
+          const int pages = (vhi + kPage - 1) / kPage;
+          if (dead) return false;
+          if constexpr (!C::kCodes) {
+            // lane 2 i + half copies that half of page i's rows
+            int pg = 0;
+            if ((lane >> 1) < pages && lane < 2 * BPAGES) {
+              pg = table[key0 / kPage + (lane >> 1)];
+              if (pg < 0 || pg >= p.c.pool_pages) {
+                set_status(p.c.status, SDV_ERR_PAGE_RANGE);
+                pg = 0;
+              }
+            }
+            const bool mine = lane < C::HALVES * BPAGES;
+            const int pgi = C::HALVES == 2 ? lane >> 1 : lane, half = C::HALVES == 2 ? lane & 1 : 0;
+            const int page = __shfl_sync(0xffffffffu, pg, (2 * pgi) & 31);
+#pragma unroll
+            for (int kv = 0; kv < 2; ++kv) {
+              wait(&empty[slot], phase ^ 1);
+              if (dead) return false;
+              uint8_t* dst = smem + slot * C::SLOT;
+              const bool cut = kv == 1 && (vlo > 0 || vhi < BK);
+              uint64_t* bar = cut ? tail : &full[slot];
+              if (lane == 0) mbar_arrive_expect_tx(bar, pages * C::HALVES * 2048);
+              __syncwarp();
+              if (mine && pgi < pages) tma_load_5d(dst + half * HALF + pgi * 2048, &tmKV, bar, half * 64, 0, kv, h, page);
+              if (cut) {
+                // zero the values of keys that are not seen: they may be anything
+                wait(tail, tail_phase);
+                tail_phase ^= 1;
+                for (int r = lane >> 3; r < BK; r += 4)
+                  if (r < vlo || r >= vhi)
+#pragma unroll
+                    for (int hf = 0; hf < C::HALVES; ++hf)
+                      *reinterpret_cast<uint4*>(dst + hf * HALF + r * 128 + (lane & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&full[slot]);
+              }
+              if (++slot == C::NS) {
+                slot = 0;
+                phase ^= 1;
+              }
+            }
+          } else {
+            // 8 lanes (4 with 64 columns) a row, 16 codes each
+            constexpr int LANES = D / 16, STEP = 128 / LANES;
+            const int ct = tid - CONV_WARP * kWarp, ch = ct % LANES, r0 = ct / LANES;
+            constexpr int NR = BK / STEP;  // rows a thread takes
+#pragma unroll
+            for (int kv = 0; kv < 2; ++kv) {
+              uint4 w[NR];
+              uint32_t sc[NR];
+#pragma unroll
+              for (int i = 0; i < NR; ++i) {
+                const int r = r0 + i * STEP;
+                w[i] = make_uint4(0u, 0u, 0u, 0u);
+                sc[i] = 127;
+                if (r >= vlo && r < vhi) {
+                  const int pg = table[(key0 + r) / kPage];
+                  if (pg < 0 || pg >= p.c.pool_pages) {
+                    set_status(p.c.status, SDV_ERR_PAGE_RANGE);
+                  } else {
+                    const long long place = (((long long)pg * n_kv + h) * 2 + kv) * kPage + (key0 + r) % kPage;
+                    w[i] = *reinterpret_cast<const uint4*>(p.c.pool + place * D + ch * 16);
+                    sc[i] = p.c.scales[place];
+                  }
+                }
+              }
+              wait(&empty[slot], phase ^ 1);
+              if (dead) return false;
+              uint8_t* dst = smem + slot * C::SLOT + (ch >> 2) * HALF;
+#pragma unroll
+              for (int i = 0; i < NR; ++i) {
+                const int r = r0 + i * STEP;
+                // 2^e in fp16, below its normal range for e = -15
+                const int e = static_cast<int>(sc[i]) - 127;
+                const uint32_t bits = e >= -14 ? static_cast<uint32_t>(e + 15) << 10 : 0x200u;
+                const uint32_t pair = bits | (bits << 16);
+                const __half2 m = *reinterpret_cast<const __half2*>(&pair);
+                const uint32_t ws[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+                uint32_t o[8];
+#pragma unroll
+                for (int x = 0; x < 8; ++x) {
+                  const uint32_t c2 = e4m3x2_to_f16x2(ws[x >> 1] >> (16 * (x & 1)));
+                  const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&c2), m);
+                  o[x] = *reinterpret_cast<const uint32_t*>(&y);
+                }
+                const int c0 = (ch & 3) * 2, f = (ch >> 2) & 1;  // upper halves store their second chunk first: no bank meets twice
+                uint8_t* row = dst + r * 128;
+                const uint4 a = make_uint4(o[0], o[1], o[2], o[3]), c = make_uint4(o[4], o[5], o[6], o[7]);
+                *reinterpret_cast<uint4*>(row + (((c0 + f) ^ (r & 7)) << 4)) = f ? c : a;
+                *reinterpret_cast<uint4*>(row + (((c0 + 1 - f) ^ (r & 7)) << 4)) = f ? a : c;
+              }
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&full[slot]);
+              if (++slot == C::NS) {
+                slot = 0;
+                phase ^= 1;
+              }
+            }
+          }
+        }
+        return true;
+      });
+      // no copy may be in flight when the block ends: every slot has been read
+      if constexpr (!C::kCodes) {
+        for (int i = 0; i < C::NS && !dead; ++i) {
+          wait(&empty[slot], phase ^ 1);
+          if (++slot == C::NS) {
+            slot = 0;
+            phase ^= 1;
+          }
+        }
+      }
+    }
+  };
+  auto multiply = [&]() {
+    // ---------------- products ----------------
+    if (lane == 0) {
+      constexpr uint32_t id_s = idesc(C::kCodes, BK, false), id_o = idesc(C::kCodes, D, true);
+      const uint32_t sm = smem_u32(smem);
+      int slot = 0;  // the slot of the next block's K; its V follows
+      uint32_t phase = 0;
+      uint32_t pph[2] = {0, 0}, qph[2] = {0, 0};
+      bool dead = dead0;
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (!dead && !mbar_wait(bar, parity)) {
+          set_status(p.c.status, SDV_ERR_TIMEOUT);
+          dead = true;
+        }
+        tc_fence_after();
+      };
+      walk([&](const SeqRows& s, int, int, const Item& it, long long, int b0, int b1) {
+        const Tile t[2] = {clip(make_tile(s, it, group, window, 0), b0, b1), clip(make_tile(s, it, group, window, 1), b0, b1)};
+        int vslot = 0;
+        uint32_t vphase = 0;
+        bool had = false;  // block j - 1 was loaded
+        for (int j = b0; j <= b1; ++j) {
+          if (dead) return false;
+          const bool has = j < b1 && ((j >= t[0].b0 && j < t[0].b1) || (j >= t[1].b0 && j < t[1].b1));
+          bool k_in = false, v_in = false;
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            if (had && j - 1 >= t[x].b0 && j - 1 < t[x].b1) {
+              if (!v_in) wait(&full[vslot], vphase);
+              v_in = true;
+              wait(&p_full[x], pph[x]);
+              pph[x] ^= 1;
+              if (dead) return false;
+              const uint32_t vb = sm + vslot * C::SLOT;
+#pragma unroll
+              for (int k = 0; k < BK / 16; ++k)
+                umma_ts(tmem + C::T_O + x * D, tmem + x * BK + k * 8, desc_mn(vb + k * 2048), id_o, j - 1 == t[x].b0 && k == 0 ? 0u : 1u);
+              if (j == t[x].b1) umma_commit(&o_full[x]);
+            }
+            if (has && j >= t[x].b0 && j < t[x].b1) {
+              if (!k_in) wait(&full[slot], phase);
+              k_in = true;
+              if (j == t[x].b0) {
+                wait(&q_full[x], qph[x]);
+                qph[x] ^= 1;
+              }
+              if (dead) return false;
+              const uint32_t kb = sm + slot * C::SLOT, qb = sm + C::OFF_Q + x * C::SLOT;
+#pragma unroll
+              for (int k = 0; k < D / 16; ++k)
+                umma_bf16(tmem + x * BK, desc_sw128(qb + (k >> 2) * HALF + (k & 3) * 32), desc_sw128(kb + (k >> 2) * HALF + (k & 3) * 32), id_s,
+                          k == 0 ? 0u : 1u);
+              umma_commit(&s_full[x]);
+            }
+          }
+          if (had) umma_commit(&empty[vslot]);
+          had = has;
+          if (has) {
+            umma_commit(&empty[slot]);
+            if (++slot == C::NS) {
+              slot = 0;
+              phase ^= 1;
+            }
+            vslot = slot;
+            vphase = phase;
+            if (++slot == C::NS) {
+              slot = 0;
+              phase ^= 1;
+            }
+          }
+        }
+        return true;
+      });
+      // every product has ended before the block gives its TMEM back
+      umma_commit(done);
+      if (!mbar_wait(done, 0)) set_status(p.c.status, SDV_ERR_TIMEOUT);
+    }
+    __syncwarp();
+  };
+  auto softmax = [&]() {
+    // ---------------- softmax, output: four warps a tile, a thread a row ----------------
+    const int t = warp >> 2, i = tid & (BM - 1);
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t t_s = tmem + lanes + t * BK, t_o = tmem + lanes + C::T_O + t * D;
+    uint32_t sph = 0, oph = 0;
+    bool dead = dead0;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      if (!dead && !mbar_wait(bar, parity)) {
+        set_status(p.c.status, SDV_ERR_TIMEOUT);
+        dead = true;
+      }
+      dead = __any_sync(0xffffffffu, dead);
+      tc_fence_after();
+    };
+    walk([&](const SeqRows& s, int, int h, const Item& it, long long u0, int b0, int b1) {
+      const Tile whole = make_tile(s, it, group, window, t), x = clip(whole, b0, b1);
+      const int row = it.row0 + t * BM + i;
+      const bool in = i < whole.rows;
+      const int pos = in ? s.pos0 + row / group : -1;
+      const long long tok = s.off + (in ? row / group : 0);
+      const int head = h * group + (in ? row % group : 0);
+      float cz = p.scale_log2, m = kNoMax, l = 0.f;
+      if (x.b0 < x.b1 && !dead) {
+        // this row's query into the tile (its last reader, the item before, is done: its scores were all read)
+        const uint4* src = reinterpret_cast<const uint4*>(p.q + tok * p.q_stride + (long long)head * D);
+        uint8_t* dst = smem + C::OFF_Q + t * C::SLOT + i * 128;
+        uint4 w[D / 8];
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) w[c] = in ? src[c] : make_uint4(0u, 0u, 0u, 0u);
+        if constexpr (C::kCodes) {
+          // fp16 with the row's largest magnitude in [1/2, 1)
+          float a = 0.f;
+#pragma unroll
+          for (int c = 0; c < D / 8; ++c) {
+            const uint32_t* v = &w[c].x;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) a = fmaxf(a, fmaxf(fabsf(__uint_as_float(v[k] << 16)), fabsf(__uint_as_float(v[k] & 0xFFFF0000u))));
+          }
+          const int e = min(max(static_cast<int>(__float_as_uint(a) >> 23) - 126, -100), 100);
+          const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+          cz *= __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+#pragma unroll
+          for (int c = 0; c < D / 8; ++c) {
+            uint32_t* v = &w[c].x;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const __half2 y = __floats2half2_rn(__uint_as_float(v[k] << 16) * inv, __uint_as_float(v[k] & 0xFFFF0000u) * inv);
+              v[k] = *reinterpret_cast<const uint32_t*>(&y);
+            }
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) *reinterpret_cast<uint4*>(dst + (c >> 3) * HALF + (((c & 7) ^ (i & 7)) << 4)) = w[c];
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_full[t]);
+      }
+      for (int j = x.b0; j < x.b1; ++j) {
+        wait(&s_full[t], sph);
+        sph ^= 1;
+        if (dead) break;
+        const int key0 = it.page_lo * kPage + j * BK;
+        const bool full_block = key0 + BK - 1 <= x.pmin && (window <= 0 || key0 > x.pmax - window);
+        const int rel = pos - key0;  // key column c is seen when c <= rel and c > rel - window
+        const int low = window > 0 ? rel - window : -0x40000000;
+        uint32_t buf[2][32];
+        auto mask = [&](uint32_t (&r)[32], int c0) {
+          if (!full_block) {
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if (c0 + c > rel || c0 + c <= low) r[c] = 0xFF800000u;
+          }
+        };
+        auto top32 = [&](const uint32_t (&r)[32], float v) {
+#pragma unroll
+          for (int c = 0; c < 32; c += 2) v = fmaxf(v, fmaxf(__uint_as_float(r[c]), __uint_as_float(r[c + 1])));
+          return v;
+        };
+        if (j == x.b0) {  // the first block sets the bound
+          float top = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            tmem_ld32(t_s + 32 * c, buf[0]);
+            tmem_wait_ld(buf[0]);
+            mask(buf[0], 32 * c);
+            top = top32(buf[0], top);
+          }
+          m = fmaxf(kNoMax, top * cz);
+        }
+        uint32_t pw[2][32];
+        for (;;) {
+          float top = -INFINITY;
+          uint64_t sum[2] = {0, 0};
+          const uint64_t cc = f2(cz, cz), mm = f2(-m, -m);
+          tmem_ld32(t_s, buf[0]);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            tmem_wait_ld(buf[c & 1]);
+            if (c < 3) tmem_ld32(t_s + 32 * (c + 1), buf[(c + 1) & 1]);
+            uint32_t (&r)[32] = buf[c & 1];
+            mask(r, 32 * c);
+            top = top32(r, top);
+#pragma unroll
+            for (int k = 0; k < 32; k += 2) {
+              float a, b;
+              unf2(fma2(f2(__uint_as_float(r[k]), __uint_as_float(r[k + 1])), cc, mm), a, b);
+              a = fast_ex2(a);
+              b = fast_ex2(b);
+              sum[(k >> 1) & 1] = add2(sum[(k >> 1) & 1], f2(a, b));
+              if constexpr (C::kCodes) {
+                const __half2 y = __floats2half2_rn(a, b);
+                pw[c >> 1][(c & 1) * 16 + (k >> 1)] = *reinterpret_cast<const uint32_t*>(&y);
+              } else {
+                pw[c >> 1][(c & 1) * 16 + (k >> 1)] = pack_bf16x2(a, b);
+              }
+            }
+          }
+          const float z = top * cz;
+          if (!__any_sync(0xffffffffu, z > m + kSlack)) {
+            float a, b;
+            unf2(add2(sum[0], sum[1]), a, b);
+            l += a + b;
+            break;
+          }
+          // move the bounds that are passed and take the block again
+          const float mn = z > m + kSlack ? z : m, f = fast_ex2(m - mn);
+          m = mn;
+          l *= f;
+          if (j > x.b0) {
+            const uint64_t ff = f2(f, f);
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+              tmem_ld32(t_o + 32 * c, buf[0]);
+              tmem_wait_ld(buf[0]);
+#pragma unroll
+              for (int k = 0; k < 32; k += 2) {
+                float a, b;
+                unf2(mul2(f2(__uint_as_float(buf[0][k]), __uint_as_float(buf[0][k + 1])), ff), a, b);
+                buf[0][k] = __float_as_uint(a);
+                buf[0][k + 1] = __float_as_uint(b);
+              }
+              tmem_st32(t_o + 32 * c, buf[0]);
+            }
+            tmem_wait_st();
+          }
+        }
+        tmem_st32(t_s, pw[0]);
+        tmem_st32(t_s + 32, pw[1]);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[t]);
+      }
+      if (x.b0 < x.b1) {
+        wait(&o_full[t], oph);
+        oph ^= 1;
+      }
+      // the blocks that hold a part of this item
+      const int c_first = static_cast<int>(u0 / per_cta), c_last = static_cast<int>((u0 + it.blocks - 1) / per_cta);
+      __nv_bfloat16* dst = p.out + tok * p.out_stride + (long long)head * D;
+      if (c_first == c_last) {
+        const float inv = l == 0.f ? 0.f : 1.f / l;  // a row that sees nothing gives 0
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t r[32];
+          if (x.b0 < x.b1 && !dead) {
+            tmem_ld32(t_o + 32 * c, r);
+            tmem_wait_ld(r);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) r[k] = 0;
+          }
+          if (in && !dead)
+#pragma unroll
+            for (int k = 0; k < 32; k += 8) {
+              uint32_t o[4];
+#pragma unroll
+              for (int y = 0; y < 4; ++y)
+                o[y] = l == 0.f ? 0u : pack_bf16x2(__uint_as_float(r[k + 2 * y]) * inv, __uint_as_float(r[k + 2 * y + 1]) * inv);
+              *reinterpret_cast<uint4*>(dst + 32 * c + k) = make_uint4(o[0], o[1], o[2], o[3]);
+            }
+        }
+        tc_fence_before();
+        return true;
+      }
+      // a part: [column][row], then bounds and sums; slot 0 for an item begun before this run, 1 for one that goes on
+      constexpr long long PF = (long long)BM * (D + 2);
+      auto part_of = [&](int cta) { return p.part + ((2LL * cta + (cta == c_first)) * 2 + t) * PF; };
+      float* mine = part_of(blockIdx.x);
+      if (x.b0 < x.b1 && !dead) {
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t r[32];
+          tmem_ld32(t_o + 32 * c, r);
+          tmem_wait_ld(r);
+#pragma unroll
+          for (int k = 0; k < 32; ++k) mine[(32 * c + k) * BM + i] = __uint_as_float(r[k]);
+        }
+        tc_fence_before();
+      }
+      mine[D * BM + i] = m;
+      mine[(D + 1) * BM + i] = l;
+      __threadfence();
+      named_sync(1 + t, BM);
+      int* s_last = reinterpret_cast<int*>(tmem_slot + 1 + t);
+      if (i == 0) {
+        int* count = p.counters + 2 * c_first + t;
+        *s_last = atomicAdd(count, 1) == c_last - c_first;
+        if (*s_last) *count = 0;
+        __threadfence();
+      }
+      named_sync(1 + t, BM);
+      const bool last = *reinterpret_cast<volatile int*>(s_last) != 0;
+      named_sync(1 + t, BM);  // read by all before the next item writes it
+      if (!last || dead || !in) return true;
+      m = kNoMax;
+      for (int cta = c_first; cta <= c_last; ++cta) m = fmaxf(m, __ldcg(part_of(cta) + D * BM + i));
+      l = 0.f;
+      for (int cta = c_first; cta <= c_last; ++cta)
+        l += fast_ex2(__ldcg(part_of(cta) + D * BM + i) - m) * __ldcg(part_of(cta) + (D + 1) * BM + i);
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        float acc[32];
+#pragma unroll
+        for (int k = 0; k < 32; ++k) acc[k] = 0.f;
+        for (int cta = c_first; cta <= c_last; ++cta) {
+          const float* src = part_of(cta);
+          if (__ldcg(src + (D + 1) * BM + i) == 0.f) continue;  // it saw nothing and wrote no columns
+          const float f = fast_ex2(__ldcg(src + D * BM + i) - m) * inv;
+#pragma unroll
+          for (int k = 0; k < 32; ++k) acc[k] += f * __ldcg(src + (32 * c + k) * BM + i);
+        }
+#pragma unroll
+        for (int k = 0; k < 32; k += 8)
+          *reinterpret_cast<uint4*>(dst + 32 * c + k) = make_uint4(pack_bf16x2(acc[k], acc[k + 1]), pack_bf16x2(acc[k + 2], acc[k + 3]),
+                                                                   pack_bf16x2(acc[k + 4], acc[k + 5]), pack_bf16x2(acc[k + 6], acc[k + 7]));
+      }
+      return true;
+    });
+  };
+  // a warpgroup changes its registers as one
+  if (warp >= CONV_WARP) {
+    regs_down<C::R_CONV>();
+    if constexpr (C::kCodes) load();
+  } else if (warp >= MMA_WARP) {
+    regs_down<C::R_ISSUE>();
+    if (warp == MMA_WARP) multiply();
+    if constexpr (!C::kCodes)
+      if (warp == TMA_WARP) load();
+  } else {
+    regs_up<C::R_SOFT>();
+    softmax();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == MMA_WARP) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  }
+}
+
+template <int D, int FMT>
+cudaError_t launch_one(const CUtensorMap& map, const ChunkAttnParams& p, int grid, cudaStream_t stream) {
+  return launch_pdl(chunk_attn_tc_kernel<D, FMT>, dim3(grid), dim3(Cfg<D, FMT>::THREADS), Cfg<D, FMT>::SMEM, stream, map, p);
+}
+
+template <int D, int FMT>
+cudaError_t setup_one() {
+  return cudaFuncSetAttribute(chunk_attn_tc_kernel<D, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D, FMT>::SMEM);
+}
+
+}  // namespace
+
+size_t chunk_attn_tc_part_floats(int head_dim, int grid) { return static_cast<size_t>(grid) * 4 * BM * (head_dim + 2); }
+
+cudaError_t setup_chunk_attn_tc(int head_dim, int cache_format) {
+  if (head_dim == 64)
+    return cache_format == SDV_CACHE_BF16 ? setup_one<64, SDV_CACHE_BF16>() : setup_one<64, SDV_CACHE_E4M3>();
+  return cache_format == SDV_CACHE_BF16 ? setup_one<128, SDV_CACHE_BF16>() : setup_one<128, SDV_CACHE_E4M3>();
+}
+
+cudaError_t launch_chunk_attn_tc(int head_dim, int cache_format, const CUtensorMap& map, const ChunkAttnParams& p, int grid,
+                                 cudaStream_t stream) {
+  if (head_dim == 64)
+    return cache_format == SDV_CACHE_BF16 ? launch_one<64, SDV_CACHE_BF16>(map, p, grid, stream)
+                                          : launch_one<64, SDV_CACHE_E4M3>(map, p, grid, stream);
+  return cache_format == SDV_CACHE_BF16 ? launch_one<128, SDV_CACHE_BF16>(map, p, grid, stream)
+                                        : launch_one<128, SDV_CACHE_E4M3>(map, p, grid, stream);
+}
+
+}  // namespace sdv

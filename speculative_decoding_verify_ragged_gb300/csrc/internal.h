@@ -305,6 +305,9 @@ struct AdmitParams {
 // Append admitted sequences to a slot table (one block).
 cudaError_t launch_admit(const AdmitParams& p, cudaStream_t stream);
 
+// bf16 KV pool [pages, n_kv, 2, 16, head_dim] as a 5-D tensor map; box = 64 of head_dim x 16 slots.
+bool encode_kv_map(CUtensorMap* m, const void* base, int n_kv, int head_dim, int pool_pages);
+
 // SDV_ERR_CUDA, with the error kept for sdv_last_cuda_error
 sdv_status cuda_fail(cudaError_t e);
 
