@@ -8,9 +8,10 @@
 //   S_t = Q_t K^T  (M = 128 rows, N = 128 keys),  O_t += P_t V  (P_t from TMEM)
 // run for tile 0 and tile 1 in turn, so the tensor cores work on one tile while
 // the other's softmax runs: one thread holds one row, reads its scores from
-// TMEM once and writes the weights over them in 16 bits.  The maximum is a
-// bound that moves only when a row's scores pass it by 2^8 (then the block is taken again and O is
-// rescaled in TMEM), so a block is one pass.
+// TMEM once and writes the weights over them in 16 bits.  The running maximum is a
+// bound, set by the first block and moved only when a block's weights add up
+// to more than kMost (then the block is taken again and O is rescaled in TMEM): their sum,
+// which is needed anyway, stands in for a maximum.
 //
 // TMEM: S_0, S_1 (128 columns each; P_t over S_t's first 64), O_0, O_1 (D each).
 // Shared memory: Q tiles and a ring of K and V blocks, rows of 128 bytes,
@@ -31,9 +32,11 @@ constexpr int BK = 128;              // keys of a block
 constexpr int BPAGES = BK / kPage;
 constexpr int HALF = BM * 128;       // 64 columns of 128 rows: 16 KB
 constexpr float kNoMax = -1e30f;     // the bound before the first visible key, in base-2 logits
-constexpr float kSlack = 8.f;        // log2 of what a weight may reach before its bound moves
+// A row's weights of one block may add up to this before its bound moves: each
+// then fits fp16, and no maximum is taken in the blocks between.
+constexpr float kMost = 16384.f;
 
-constexpr int MMA_WARP = 8, TMA_WARP = 9, CONV_WARP = 12;
+constexpr int MMA_WARP = 8, TMA_WARP = 10, CONV_WARP = 12;  // MMA_WARP + t issues tile t's products, TMA_WARP + 1 copies V
 
 template <int D, int FMT>
 struct Cfg {
@@ -44,7 +47,7 @@ struct Cfg {
   static constexpr int NS = D == 128 ? 5 : 8;
   static constexpr int OFF_Q = NS * SLOT;
   static constexpr int OFF_BAR = OFF_Q + 2 * SLOT;
-  static constexpr int NBAR = 2 * NS + 2 * 4 + 2;     // full, empty; s, p, q, o of each tile; tail, done
+  static constexpr int NBAR = 2 * NS + 2 * 4 + 4;     // full, empty; s, p, q, o of each tile; tail, turn of each, done
   static constexpr int SMEM = 1024 + OFF_BAR + NBAR * 8 + 64;
   static_assert(SMEM <= 227 * 1024, "shared memory");
   static constexpr int FULL_COUNT = kCodes ? 4 : 1;
@@ -55,15 +58,12 @@ struct Cfg {
   static constexpr int T_O = 2 * BK;                  // TMEM columns of O_0
 };
 
-__device__ __forceinline__ uint64_t desc_mn(uint32_t saddr) {  // V rows read MN-major: 16 KB between 64-column halves
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
-  d |= static_cast<uint64_t>(HALF >> 4) << 16;
-  d |= static_cast<uint64_t>(1024 >> 4) << 32;
-  d |= static_cast<uint64_t>(1) << 46;
-  d |= static_cast<uint64_t>(2) << 61;
-  return d;
-}
+// Shared-memory descriptors (128-byte swizzle, version 1) as two words: the low
+// one holds the address and is all that changes from product to product, so
+// the issuing thread adds a constant to it and nothing else.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);  // 1024 bytes between 8-row groups
+__device__ __forceinline__ uint32_t desc_k(uint32_t saddr) { return (saddr >> 4) | (1u << 16); }                        // K-major
+__device__ __forceinline__ uint32_t desc_mn(uint32_t saddr) { return (saddr >> 4) | (static_cast<uint32_t>(HALF >> 4) << 16); }  // V rows, MN-major: 16 KB between 64-column halves
 
 // fp32 accumulate; bf16 operands, or fp16 (format 0)
 __host__ __device__ constexpr uint32_t idesc(bool f16, int N, bool b_mn) {
@@ -71,14 +71,41 @@ __host__ __device__ constexpr uint32_t idesc(bool f16, int N, bool b_mn) {
          (static_cast<uint32_t>(BM >> 4) << 24);
 }
 
-__device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t id, uint32_t acc) {
+// D (+)= A B, both from shared memory; acc 0 starts D anew.
+template <uint32_t ID>
+__device__ __forceinline__ void umma_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t acc) {
   asm volatile(
       "{\n"
       " .reg .pred p;\n"
-      " setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n"
+      " .reg .b64 a, b;\n"
+      " mov.b64 a, {%1, %3};\n"
+      " mov.b64 b, {%2, %3};\n"
+      " setp.ne.b32 p, %5, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n"
       "}\n" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b), "r"(id), "r"(acc));
+      "r"(a_lo), "r"(b_lo), "n"(kDescHi), "r"(ID), "r"(acc));
+}
+// The same with A from TMEM.
+template <uint32_t ID>
+__device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t acc) {
+  asm volatile(
+      "{\n"
+      " .reg .pred p;\n"
+      " .reg .b64 b;\n"
+      " mov.b64 b, {%2, %3};\n"
+      " setp.ne.b32 p, %5, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n"
+      "}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_lo), "n"(kDescHi), "r"(ID), "r"(acc));
+}
+
+// mbar_wait with the clock read only after the barrier has been asked for a while.
+__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity) {
+  const uint32_t addr = smem_u32(bar);
+#pragma unroll 1
+  for (int i = 0; i < 64; ++i)
+    if (mbar_try_wait(addr, parity)) return true;
+  return mbar_wait(bar, parity);
 }
 
 // Registers per thread of this warpgroup (the shares of all add up to the launch's).
@@ -194,7 +221,8 @@ __global__ void __launch_bounds__(Cfg<D, FMT>::THREADS, 1)
   uint64_t* q_full = p_full + 2;     // [2]
   uint64_t* o_full = q_full + 2;     // [2] the item's last product of tile t is in O_t
   uint64_t* tail = o_full + 2;       // copies of a block whose end is zeroed before use
-  uint64_t* done = tail + 1;
+  uint64_t* turn = tail + 1;         // [2] tile t may issue its products
+  uint64_t* done = turn + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
   __shared__ long long s_scan[2];        // first unit of the sequence the run starts in; units of the launch
   __shared__ Place s_start;
@@ -203,16 +231,17 @@ __global__ void __launch_bounds__(Cfg<D, FMT>::THREADS, 1)
   if (tid == 0) {
     for (int i = 0; i < C::NS; ++i) {
       mbar_init(&full[i], C::FULL_COUNT);
-      mbar_init(&empty[i], 1);
+      mbar_init(&empty[i], 2);  // both tiles' products have read it
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&s_full[t], 1);
       mbar_init(&p_full[t], 4);
       mbar_init(&q_full[t], 4);
       mbar_init(&o_full[t], 1);
+      mbar_init(&turn[t], 1);
     }
     mbar_init(tail, 1);
-    mbar_init(done, 1);
+    mbar_init(done, 2);
     fence_barrier_init();
   }
   if (warp == MMA_WARP) {
@@ -354,212 +383,233 @@ __global__ void __launch_bounds__(Cfg<D, FMT>::THREADS, 1)
     return x;
   };
 
-  auto load = [&]() {
+  // the blocks that either tile needs: their ranges meet, for a tile's rows
+  // follow one another and so do the positions that they see
+  auto both = [](const Tile& a, const Tile& b) {
+    if (a.b0 >= a.b1) return make_int2(b.b0, b.b1);
+    if (b.b0 >= b.b1) return make_int2(a.b0, a.b1);
+    return make_int2(min(a.b0, b.b0), max(a.b1, b.b1));
+  };
+  auto load = [&](int kv0) {
     // ---------------- loads: K and V of each block into the ring, in turn ----------------
-    {
-      int slot = 0;
-      uint32_t phase = 0, tail_phase = 0;
-      bool dead = dead0;
-      auto wait = [&](uint64_t* bar, uint32_t parity) {
-        if (!dead && !mbar_wait(bar, parity)) {
-          set_status(p.c.status, SDV_ERR_TIMEOUT);
-          dead = true;
+    // bf16: one warp copies the keys (kv0 = 0), one the values; codes: four warps take both
+    constexpr int EVERY = C::kCodes ? 1 : 2;
+    int slot = kv0;
+    uint32_t phase = 0, tail_phase = 0;
+    bool dead = dead0;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      if (!dead && !bar_wait(bar, parity)) {
+        set_status(p.c.status, SDV_ERR_TIMEOUT);
+        dead = true;
+      }
+      dead = __any_sync(0xffffffffu, dead);
+    };
+    auto next = [&]() {
+      slot += EVERY;
+      if (slot >= C::NS) {
+        slot -= C::NS;
+        phase ^= 1;
+      }
+    };
+    walk([&](const SeqRows& s, int b, int h, const Item& it, long long, int b0, int b1) {
+      const Tile t0 = clip(make_tile(s, it, group, window, 0), b0, b1), t1 = clip(make_tile(s, it, group, window, 1), b0, b1);
+      const int2 used = both(t0, t1);
+      if (used.x >= used.y || dead) return !dead;
+      const int* table = p.c.page_table + (long long)b * p.c.max_pages;
+      const int page0 = it.page_lo + used.x * BPAGES, pages_end = min((it.khi + kPage - 1) / kPage, it.page_lo + used.y * BPAGES);
+      // the lanes hold the pages of four blocks, and fetch the next four's meanwhile
+      auto fetch = [&](int jj) {
+        int pg = 0;
+        if (page0 + jj * BPAGES + lane < pages_end) {
+          pg = table[page0 + jj * BPAGES + lane];
+          if (pg < 0 || pg >= p.c.pool_pages) {
+            set_status(p.c.status, SDV_ERR_PAGE_RANGE);
+            pg = 0;  // some page of the pool: the call's outputs hold nothing meaningful
+          }
         }
-        dead = __any_sync(0xffffffffu, dead);
+        return pg;
       };
-      walk([&](const SeqRows& s, int b, int h, const Item& it, long long, int b0, int b1) {
-        const Tile t0 = clip(make_tile(s, it, group, window, 0), b0, b1), t1 = clip(make_tile(s, it, group, window, 1), b0, b1);
-        const int* table = p.c.page_table + (long long)b * p.c.max_pages;
-        for (int j = b0; j < b1; ++j) {
-          if (!((j >= t0.b0 && j < t0.b1) || (j >= t1.b0 && j < t1.b1))) continue;
-          const int key0 = it.page_lo * kPage + j * BK;
-          const int vlo = max(0, it.klo - key0), vhi = min(BK, it.khi - key0);  // the block's rows that are seen
-          const int pages = (vhi + kPage - 1) / kPage;
-          if (dead) return false;
-          if constexpr (!C::kCodes) {
-            // lane 2 i + half copies that half of page i's rows
-            int pg = 0;
-            if ((lane >> 1) < pages && lane < 2 * BPAGES) {
-              pg = table[key0 / kPage + (lane >> 1)];
-              if (pg < 0 || pg >= p.c.pool_pages) {
-                set_status(p.c.status, SDV_ERR_PAGE_RANGE);
-                pg = 0;
-              }
-            }
-            const bool mine = lane < C::HALVES * BPAGES;
-            const int pgi = C::HALVES == 2 ? lane >> 1 : lane, half = C::HALVES == 2 ? lane & 1 : 0;
-            const int page = __shfl_sync(0xffffffffu, pg, (2 * pgi) & 31);
-#pragma unroll
-            for (int kv = 0; kv < 2; ++kv) {
-              wait(&empty[slot], phase ^ 1);
-              if (dead) return false;
-              uint8_t* dst = smem + slot * C::SLOT;
-              const bool cut = kv == 1 && (vlo > 0 || vhi < BK);
-              uint64_t* bar = cut ? tail : &full[slot];
-              if (lane == 0) mbar_arrive_expect_tx(bar, pages * C::HALVES * 2048);
-              __syncwarp();
-              if (mine && pgi < pages) tma_load_5d(dst + half * HALF + pgi * 2048, &tmKV, bar, half * 64, 0, kv, h, page);
-              if (cut) {
-                // zero the values of keys that are not seen: they may be anything
-                wait(tail, tail_phase);
-                tail_phase ^= 1;
-                for (int r = lane >> 3; r < BK; r += 4)
-                  if (r < vlo || r >= vhi)
-#pragma unroll
-                    for (int hf = 0; hf < C::HALVES; ++hf)
-                      *reinterpret_cast<uint4*>(dst + hf * HALF + r * 128 + (lane & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&full[slot]);
-              }
-              if (++slot == C::NS) {
-                slot = 0;
-                phase ^= 1;
-              }
-            }
-          } else {
-            // 8 lanes (4 with 64 columns) a row, 16 codes each
-            constexpr int LANES = D / 16, STEP = 128 / LANES;
-            const int ct = tid - CONV_WARP * kWarp, ch = ct % LANES, r0 = ct / LANES;
-            constexpr int NR = BK / STEP;  // rows a thread takes
-#pragma unroll
-            for (int kv = 0; kv < 2; ++kv) {
-              uint4 w[NR];
-              uint32_t sc[NR];
-#pragma unroll
-              for (int i = 0; i < NR; ++i) {
-                const int r = r0 + i * STEP;
-                w[i] = make_uint4(0u, 0u, 0u, 0u);
-                sc[i] = 127;
-                if (r >= vlo && r < vhi) {
-                  const int pg = table[(key0 + r) / kPage];
-                  if (pg < 0 || pg >= p.c.pool_pages) {
-                    set_status(p.c.status, SDV_ERR_PAGE_RANGE);
-                  } else {
-                    const long long place = (((long long)pg * n_kv + h) * 2 + kv) * kPage + (key0 + r) % kPage;
-                    w[i] = *reinterpret_cast<const uint4*>(p.c.pool + place * D + ch * 16);
-                    sc[i] = p.c.scales[place];
-                  }
-                }
-              }
-              wait(&empty[slot], phase ^ 1);
-              if (dead) return false;
-              uint8_t* dst = smem + slot * C::SLOT + (ch >> 2) * HALF;
-#pragma unroll
-              for (int i = 0; i < NR; ++i) {
-                const int r = r0 + i * STEP;
-                // 2^e in fp16, below its normal range for e = -15
-                const int e = static_cast<int>(sc[i]) - 127;
-                const uint32_t bits = e >= -14 ? static_cast<uint32_t>(e + 15) << 10 : 0x200u;
-                const uint32_t pair = bits | (bits << 16);
-                const __half2 m = *reinterpret_cast<const __half2*>(&pair);
-                const uint32_t ws[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-                uint32_t o[8];
-#pragma unroll
-                for (int x = 0; x < 8; ++x) {
-                  const uint32_t c2 = e4m3x2_to_f16x2(ws[x >> 1] >> (16 * (x & 1)));
-                  const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&c2), m);
-                  o[x] = *reinterpret_cast<const uint32_t*>(&y);
-                }
-                const int c0 = (ch & 3) * 2, f = (ch >> 2) & 1;  // upper halves store their second chunk first: no bank meets twice
-                uint8_t* row = dst + r * 128;
-                const uint4 a = make_uint4(o[0], o[1], o[2], o[3]), c = make_uint4(o[4], o[5], o[6], o[7]);
-                *reinterpret_cast<uint4*>(row + (((c0 + f) ^ (r & 7)) << 4)) = f ? c : a;
-                *reinterpret_cast<uint4*>(row + (((c0 + 1 - f) ^ (r & 7)) << 4)) = f ? a : c;
-              }
-              fence_proxy_async_smem();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&full[slot]);
-              if (++slot == C::NS) {
-                slot = 0;
-                phase ^= 1;
-              }
-            }
-          }
-        }
-        return true;
-      });
-      // no copy may be in flight when the block ends: every slot has been read
+      int ids = fetch(0), ids_next = fetch(4);
+      auto seen = [&](int jj) {  // the rows [x, y) of block jj that are seen
+        const int key0 = (page0 + jj * BPAGES) * kPage;
+        return make_int2(max(0, it.klo - key0), min(BK, it.khi - key0));
+      };
+      const int n = used.y - used.x;
       if constexpr (!C::kCodes) {
-        for (int i = 0; i < C::NS && !dead; ++i) {
-          wait(&empty[slot], phase ^ 1);
-          if (++slot == C::NS) {
-            slot = 0;
-            phase ^= 1;
+        for (int jj = 0; jj < n; ++jj) {
+          if (jj && (jj & 3) == 0) {
+            ids = ids_next;
+            ids_next = fetch(jj + 4);
           }
+          const int2 rows = seen(jj);
+          const int pages = (rows.y + kPage - 1) / kPage;
+          // lane 2 i + half copies that half of page i's rows
+          const int pgi = C::HALVES == 2 ? lane >> 1 : lane, half = C::HALVES == 2 ? lane & 1 : 0;
+          const int page = __shfl_sync(0xffffffffu, ids, ((jj & 3) * BPAGES + pgi) & 31);
+          wait(&empty[slot], phase ^ 1);
+          if (dead) return false;
+          uint8_t* dst = smem + slot * C::SLOT;
+          const bool cut = kv0 == 1 && (rows.x > 0 || rows.y < BK);
+          uint64_t* bar = cut ? tail : &full[slot];
+          if (lane == 0) mbar_arrive_expect_tx(bar, pages * C::HALVES * 2048);
+          __syncwarp();
+          if (pgi < pages) tma_load_5d(dst + half * HALF + pgi * 2048, &tmKV, bar, half * 64, 0, kv0, h, page);
+          if (cut) {
+            // zero the values of keys that are not seen: they may be anything
+            wait(tail, tail_phase);
+            tail_phase ^= 1;
+            for (int r = lane >> 3; r < BK; r += 4)
+              if (r < rows.x || r >= rows.y)
+#pragma unroll
+                for (int hf = 0; hf < C::HALVES; ++hf)
+                  *reinterpret_cast<uint4*>(dst + hf * HALF + r * 128 + (lane & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&full[slot]);
+          }
+          next();
+        }
+      } else {
+        // 8 lanes (4 with 64 columns) a row, 16 codes each; a row's next codes
+        // are asked for as soon as its last ones are stored
+        constexpr int LANES = D / 16, STEP = 128 / LANES, NR = BK / STEP;
+        const int ct = tid - CONV_WARP * kWarp, ch = ct % LANES, r0 = ct / LANES;
+        uint4 w[NR];
+        uint32_t sc[NR];
+        auto ask = [&](int jj, int kv, int2 rows, int i) {
+          const int r = r0 + i * STEP;
+          const int page = __shfl_sync(0xffffffffu, ids, ((jj & 3) * BPAGES + (r >> 4)) & 31);
+          w[i] = make_uint4(0u, 0u, 0u, 0u);
+          sc[i] = 127;
+          if (r >= rows.x && r < rows.y) {
+            const long long place = (((long long)page * n_kv + h) * 2 + kv) * kPage + (r & 15);
+            w[i] = *reinterpret_cast<const uint4*>(p.c.pool + place * D + ch * 16);
+            sc[i] = p.c.scales[place];
+          }
+        };
+        {
+          const int2 rows = seen(0);
+#pragma unroll
+          for (int i = 0; i < NR; ++i) ask(0, 0, rows, i);
+        }
+        for (int tile = 0; tile < 2 * n; ++tile) {
+          const int jn = (tile + 1) >> 1, kvn = (tile + 1) & 1;
+          if (kvn == 0 && (jn & 3) == 0) {
+            ids = ids_next;
+            ids_next = fetch(jn + 4);
+          }
+          const int2 rows = jn < n ? seen(jn) : make_int2(0, 0);
+          wait(&empty[slot], phase ^ 1);
+          if (dead) return false;
+          uint8_t* dst = smem + slot * C::SLOT + (ch >> 2) * HALF;
+#pragma unroll
+          for (int i = 0; i < NR; ++i) {
+            const int r = r0 + i * STEP;
+            // 2^e in fp16, below its normal range for e = -15
+            const int e = static_cast<int>(sc[i]) - 127;
+            const uint32_t bits = e >= -14 ? static_cast<uint32_t>(e + 15) << 10 : 0x200u;
+            const uint32_t pair = bits | (bits << 16);
+            const __half2 m = *reinterpret_cast<const __half2*>(&pair);
+            const uint32_t ws[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+            uint32_t o[8];
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+              const uint32_t c2 = e4m3x2_to_f16x2(ws[x >> 1] >> (16 * (x & 1)));
+              const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&c2), m);
+              o[x] = *reinterpret_cast<const uint32_t*>(&y);
+            }
+            const int c0 = (ch & 3) * 2, f = (ch >> 2) & 1;  // upper halves store their second chunk first: no bank meets twice
+            uint8_t* row = dst + r * 128;
+            const uint4 a = make_uint4(o[0], o[1], o[2], o[3]), c = make_uint4(o[4], o[5], o[6], o[7]);
+            *reinterpret_cast<uint4*>(row + (((c0 + f) ^ (r & 7)) << 4)) = f ? c : a;
+            *reinterpret_cast<uint4*>(row + (((c0 + 1 - f) ^ (r & 7)) << 4)) = f ? a : c;
+            ask(jn, kvn, rows, i);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&full[slot]);
+          next();
         }
       }
-    }
+      return true;
+    });
+    // (the products wait for every slot's copies, and the block for the products:
+    // no copy is in flight when it ends)
   };
-  auto multiply = [&]() {
-    // ---------------- products ----------------
+  auto multiply = [&](int t) {
+    // ---------------- tile t's products, one thread ----------------
     if (lane == 0) {
       constexpr uint32_t id_s = idesc(C::kCodes, BK, false), id_o = idesc(C::kCodes, D, true);
-      const uint32_t sm = smem_u32(smem);
-      int slot = 0;  // the slot of the next block's K; its V follows
-      uint32_t phase = 0;
-      uint32_t pph[2] = {0, 0}, qph[2] = {0, 0};
+      const uint32_t d_s = tmem + t * BK, d_o = tmem + C::T_O + t * D;
+      const uint32_t ring_k = desc_k(smem_u32(smem)), ring_v = desc_mn(smem_u32(smem)), q_lo = desc_k(smem_u32(smem) + C::OFF_Q + t * C::SLOT);
+      int slot = 0;
+      uint32_t phase = 0, pph = 0, qph = 0, tph = t ? 0 : 1;  // tile 0 has the first turn
       bool dead = dead0;
       auto wait = [&](uint64_t* bar, uint32_t parity) {
-        if (!dead && !mbar_wait(bar, parity)) {
+        if (!dead && !bar_wait(bar, parity)) {
           set_status(p.c.status, SDV_ERR_TIMEOUT);
           dead = true;
         }
-        tc_fence_after();
+      };
+      auto next = [&]() {
+        if (++slot == C::NS) {
+          slot = 0;
+          phase ^= 1;
+        }
       };
       walk([&](const SeqRows& s, int, int, const Item& it, long long, int b0, int b1) {
-        const Tile t[2] = {clip(make_tile(s, it, group, window, 0), b0, b1), clip(make_tile(s, it, group, window, 1), b0, b1)};
+        const Tile t0 = clip(make_tile(s, it, group, window, 0), b0, b1), t1 = clip(make_tile(s, it, group, window, 1), b0, b1);
+        const int2 used = both(t0, t1);
+        const int first = t ? t1.b0 : t0.b0, last = t ? t1.b1 : t0.b1;
+        // step j: P of block j - 1 times its V, then S of block j.  The tiles
+        // take turns a step at a time, so that one's products run without a
+        // break while the other's softmax works: left to themselves the two
+        // fall into step, and both wait for products, then both for softmax
         int vslot = 0;
         uint32_t vphase = 0;
-        bool had = false;  // block j - 1 was loaded
-        for (int j = b0; j <= b1; ++j) {
-          if (dead) return false;
-          const bool has = j < b1 && ((j >= t[0].b0 && j < t[0].b1) || (j >= t[1].b0 && j < t[1].b1));
-          bool k_in = false, v_in = false;
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            if (had && j - 1 >= t[x].b0 && j - 1 < t[x].b1) {
-              if (!v_in) wait(&full[vslot], vphase);
-              v_in = true;
-              wait(&p_full[x], pph[x]);
-              pph[x] ^= 1;
-              if (dead) return false;
-              const uint32_t vb = sm + vslot * C::SLOT;
-#pragma unroll
-              for (int k = 0; k < BK / 16; ++k)
-                umma_ts(tmem + C::T_O + x * D, tmem + x * BK + k * 8, desc_mn(vb + k * 2048), id_o, j - 1 == t[x].b0 && k == 0 ? 0u : 1u);
-              if (j == t[x].b1) umma_commit(&o_full[x]);
-            }
-            if (has && j >= t[x].b0 && j < t[x].b1) {
-              if (!k_in) wait(&full[slot], phase);
-              k_in = true;
-              if (j == t[x].b0) {
-                wait(&q_full[x], qph[x]);
-                qph[x] ^= 1;
-              }
-              if (dead) return false;
-              const uint32_t kb = sm + slot * C::SLOT, qb = sm + C::OFF_Q + x * C::SLOT;
-#pragma unroll
-              for (int k = 0; k < D / 16; ++k)
-                umma_bf16(tmem + x * BK, desc_sw128(qb + (k >> 2) * HALF + (k & 3) * 32), desc_sw128(kb + (k >> 2) * HALF + (k & 3) * 32), id_s,
-                          k == 0 ? 0u : 1u);
-              umma_commit(&s_full[x]);
-            }
+        for (int j = used.x; j <= used.y; ++j) {
+          // (a slot is waited for even where the tile skips it: arriving on its
+          // empty barrier a round early would count twice)
+          const bool has_v = j > used.x, has_k = j < used.y;
+          const bool pv = has_v && j > first && j <= last, qk = has_k && j >= first && j < last;
+          if (has_v) wait(&full[vslot], vphase);
+          if (has_k) wait(&full[slot], phase);
+          if (qk && j == first) {
+            wait(&q_full[t], qph);
+            qph ^= 1;
           }
-          if (had) umma_commit(&empty[vslot]);
-          had = has;
-          if (has) {
-            umma_commit(&empty[slot]);
-            if (++slot == C::NS) {
-              slot = 0;
-              phase ^= 1;
+          wait(&turn[t], tph);
+          tph ^= 1;
+          if (pv) {
+            wait(&p_full[t], pph);
+            pph ^= 1;
+          }
+          if (dead) return false;
+          tc_fence_after();
+          if (pv) {
+            const uint32_t vb = ring_v + vslot * (C::SLOT >> 4);
+            umma_ts<id_o>(d_o, d_s, vb, j - 1 == first ? 0u : 1u);
+#pragma unroll
+            for (int k = 1; k < BK / 16; ++k) umma_ts<id_o>(d_o, d_s + k * 8, vb + k * (2048 >> 4), 1u);
+          }
+          if (qk) {
+            const uint32_t kb = ring_k + slot * (C::SLOT >> 4);
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+              const uint32_t off = ((k >> 2) * HALF + (k & 3) * 32) >> 4;
+              umma_ss<id_s>(d_s, q_lo + off, kb + off, k == 0 ? 0u : 1u);
             }
+            umma_commit(&s_full[t]);
+          }
+          mbar_arrive(&turn[1 - t]);
+          if (pv && j == last) umma_commit(&o_full[t]);
+          if (has_v) umma_commit(&empty[vslot]);
+          if (has_k) {
+            umma_commit(&empty[slot]);
+            next();
             vslot = slot;
             vphase = phase;
-            if (++slot == C::NS) {
-              slot = 0;
-              phase ^= 1;
-            }
+            next();
           }
         }
         return true;
@@ -578,7 +628,7 @@ __global__ void __launch_bounds__(Cfg<D, FMT>::THREADS, 1)
     uint32_t sph = 0, oph = 0;
     bool dead = dead0;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
-      if (!dead && !mbar_wait(bar, parity)) {
+      if (!dead && !bar_wait(bar, parity)) {
         set_status(p.c.status, SDV_ERR_TIMEOUT);
         dead = true;
       }
@@ -644,25 +694,21 @@ __global__ void __launch_bounds__(Cfg<D, FMT>::THREADS, 1)
               if (c0 + c > rel || c0 + c <= low) r[c] = 0xFF800000u;
           }
         };
-        auto top32 = [&](const uint32_t (&r)[32], float v) {
-#pragma unroll
-          for (int c = 0; c < 32; c += 2) v = fmaxf(v, fmaxf(__uint_as_float(r[c]), __uint_as_float(r[c + 1])));
-          return v;
-        };
-        if (j == x.b0) {  // the first block sets the bound
-          float top = -INFINITY;
+        auto row_top = [&]() {  // the block's largest logit
+          float v = -INFINITY;
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             tmem_ld32(t_s + 32 * c, buf[0]);
             tmem_wait_ld(buf[0]);
             mask(buf[0], 32 * c);
-            top = top32(buf[0], top);
+#pragma unroll
+            for (int k = 0; k < 32; k += 2) v = fmaxf(v, fmaxf(__uint_as_float(buf[0][k]), __uint_as_float(buf[0][k + 1])));
           }
-          m = fmaxf(kNoMax, top * cz);
-        }
+          return v * cz;
+        };
+        if (j == x.b0) m = fmaxf(kNoMax, row_top());  // the first block sets the bound
         uint32_t pw[2][32];
-        for (;;) {
-          float top = -INFINITY;
+        for (int again = 0;; ++again) {
           uint64_t sum[2] = {0, 0};
           const uint64_t cc = f2(cz, cz), mm = f2(-m, -m);
           tmem_ld32(t_s, buf[0]);
@@ -672,7 +718,6 @@ __global__ void __launch_bounds__(Cfg<D, FMT>::THREADS, 1)
             if (c < 3) tmem_ld32(t_s + 32 * (c + 1), buf[(c + 1) & 1]);
             uint32_t (&r)[32] = buf[c & 1];
             mask(r, 32 * c);
-            top = top32(r, top);
 #pragma unroll
             for (int k = 0; k < 32; k += 2) {
               float a, b;
@@ -688,15 +733,16 @@ __global__ void __launch_bounds__(Cfg<D, FMT>::THREADS, 1)
               }
             }
           }
-          const float z = top * cz;
-          if (!__any_sync(0xffffffffu, z > m + kSlack)) {
-            float a, b;
-            unf2(add2(sum[0], sum[1]), a, b);
-            l += a + b;
+          float total, other;
+          unf2(add2(sum[0], sum[1]), total, other);
+          total += other;
+          if (again || !__any_sync(0xffffffffu, !(total <= kMost))) {
+            l += total;
             break;
           }
-          // move the bounds that are passed and take the block again
-          const float mn = z > m + kSlack ? z : m, f = fast_ex2(m - mn);
+          // a row's weights have grown past what its bound allows (or are not
+          // numbers): move the bounds up and take the block again
+          const float mn = fmaxf(m, row_top()), f = fast_ex2(m - mn);
           m = mn;
           l *= f;
           if (j > x.b0) {
@@ -815,12 +861,12 @@ __global__ void __launch_bounds__(Cfg<D, FMT>::THREADS, 1)
   // a warpgroup changes its registers as one
   if (warp >= CONV_WARP) {
     regs_down<C::R_CONV>();
-    if constexpr (C::kCodes) load();
+    if constexpr (C::kCodes) load(0);
   } else if (warp >= MMA_WARP) {
     regs_down<C::R_ISSUE>();
-    if (warp == MMA_WARP) multiply();
+    if (warp < MMA_WARP + 2) multiply(warp - MMA_WARP);
     if constexpr (!C::kCodes)
-      if (warp == TMA_WARP) load();
+      if (warp >= TMA_WARP) load(warp - TMA_WARP);
   } else {
     regs_up<C::R_SOFT>();
     softmax();
