@@ -30,10 +30,11 @@ using namespace tc;
 constexpr int BM = 128;              // query rows of a tile
 constexpr int BK = 128;              // keys of a block
 constexpr int BPAGES = BK / kPage;
+constexpr int SK = 64;               // keys of a step: half a block
 constexpr int HALF = BM * 128;       // 64 columns of 128 rows: 16 KB
 constexpr float kNoMax = -1e30f;     // the bound before the first visible key, in base-2 logits
-// A row's weights of one block may add up to this before its bound moves: each
-// then fits fp16, and no maximum is taken in the blocks between.
+// A row's weights of one step may add up to this before its bound moves: each
+// then fits fp16, and no maximum is taken in the steps between.
 constexpr float kMost = 16384.f;
 
 constexpr int MMA_WARP = 8, TMA_WARP = 10, CONV_WARP = 12;  // MMA_WARP + t issues tile t's products, TMA_WARP + 1 copies V
@@ -47,7 +48,7 @@ struct Cfg {
   static constexpr int NS = D == 128 ? 5 : 8;
   static constexpr int OFF_Q = NS * SLOT;
   static constexpr int OFF_BAR = OFF_Q + 2 * SLOT;
-  static constexpr int NBAR = 2 * NS + 2 * 4 + 4;     // full, empty; s, p, q, o of each tile; tail, turn of each, done
+  static constexpr int NBAR = 2 * NS + 2 * 7 + 2;     // full, empty; s, p (two each), q, v, o of each tile; tail, done
   static constexpr int SMEM = 1024 + OFF_BAR + NBAR * 8 + 64;
   static_assert(SMEM <= 227 * 1024, "shared memory");
   static constexpr int FULL_COUNT = kCodes ? 4 : 1;
@@ -97,6 +98,20 @@ __device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32
       " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n"
       "}\n" ::"r"(d_tmem),
       "r"(a_tmem), "r"(b_lo), "n"(kDescHi), "r"(ID), "r"(acc));
+}
+
+// One lane of the warp, known as such to the compiler: what it issues takes its operands
+// from uniform registers (8 products of 64 columns cost 37 cycles each to issue, 70 under lane == 0).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n"
+      " .reg .pred p;\n"
+      " elect.sync _|p, 0xffffffff;\n"
+      " selp.u32 %0, 1, 0, p;\n"
+      "}\n"
+      : "=r"(r));
+  return r != 0;
 }
 
 // mbar_wait with the clock read only after the barrier has been asked for a while.
@@ -182,14 +197,14 @@ __device__ __forceinline__ Item make_item(const SeqRows& s, int group, int windo
   it.blocks = max(1, (it.khi - it.page_lo * kPage + BK - 1) / BK);
   return it;
 }
-// The item's blocks [b0, b1) that tile t needs, and its rows' range of positions.
+// The item's steps [s0, s1) that tile t needs, and its rows' range of positions.
 struct Tile {
-  int rows, pmin, pmax, b0, b1;
+  int rows, pmin, pmax, s0, s1;
 };
 __device__ __forceinline__ Tile make_tile(const SeqRows& s, const Item& it, int group, int window, int t) {
   Tile x;
   x.rows = min(BM, it.rows - t * BM);
-  x.b0 = x.b1 = 0;
+  x.s0 = x.s1 = 0;
   x.pmin = x.pmax = -1;
   if (x.rows <= 0) return x;
   const int r0 = it.row0 + t * BM;
@@ -197,8 +212,8 @@ __device__ __forceinline__ Tile make_tile(const SeqRows& s, const Item& it, int 
   x.pmax = s.pos0 + (r0 + x.rows - 1) / group;
   const int hi = x.pmax + 1, lo = window > 0 ? max(0, x.pmin - window + 1) : 0;
   if (hi <= lo || hi <= 0) return x;
-  x.b0 = (lo - it.page_lo * kPage) / BK;
-  x.b1 = (hi - it.page_lo * kPage + BK - 1) / BK;
+  x.s0 = (lo - it.page_lo * kPage) / SK;
+  x.s1 = (hi - it.page_lo * kPage + SK - 1) / SK;
   return x;
 }
 
@@ -216,13 +231,13 @@ __global__ void __launch_bounds__(Cfg<D, FMT>::THREADS, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
   uint64_t* empty = full + C::NS;
-  uint64_t* s_full = empty + C::NS;  // [2] scores of tile t are in TMEM
-  uint64_t* p_full = s_full + 2;     // [2] its weights are, and O_t may be added to
-  uint64_t* q_full = p_full + 2;     // [2]
-  uint64_t* o_full = q_full + 2;     // [2] the item's last product of tile t is in O_t
+  uint64_t* s_full = empty + C::NS;  // [tile][buffer] a step's scores are in TMEM
+  uint64_t* p_full = s_full + 4;     // [tile][buffer] its weights are, and O may be added to
+  uint64_t* q_full = p_full + 4;     // [tile]
+  uint64_t* v_done = q_full + 2;     // [tile] a step's second product is in O
+  uint64_t* o_full = v_done + 2;     // [tile] the item's last one is
   uint64_t* tail = o_full + 2;       // copies of a block whose end is zeroed before use
-  uint64_t* turn = tail + 1;         // [2] tile t may issue its products
-  uint64_t* done = turn + 2;
+  uint64_t* done = tail + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
   __shared__ long long s_scan[2];        // first unit of the sequence the run starts in; units of the launch
   __shared__ Place s_start;
@@ -234,11 +249,13 @@ __global__ void __launch_bounds__(Cfg<D, FMT>::THREADS, 1)
       mbar_init(&empty[i], 2);  // both tiles' products have read it
     }
     for (int t = 0; t < 2; ++t) {
-      mbar_init(&s_full[t], 1);
-      mbar_init(&p_full[t], 4);
+      for (int n = 0; n < 2; ++n) {
+        mbar_init(&s_full[2 * t + n], 1);
+        mbar_init(&p_full[2 * t + n], 4);
+      }
       mbar_init(&q_full[t], 4);
+      mbar_init(&v_done[t], 1);
       mbar_init(&o_full[t], 1);
-      mbar_init(&turn[t], 1);
     }
     mbar_init(tail, 1);
     mbar_init(done, 2);
@@ -251,7 +268,7 @@ __global__ void __launch_bounds__(Cfg<D, FMT>::THREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   griddep_wait();
 
   const int B = p.c.B, group = p.c.n_q / p.c.n_kv, window = p.c.window, n_kv = p.c.n_kv;
@@ -376,19 +393,19 @@ __global__ void __launch_bounds__(Cfg<D, FMT>::THREADS, 1)
       }
     }
   };
-  auto clip = [](Tile x, int b0, int b1) {  // the tile's blocks within [b0, b1)
-    x.b0 = max(x.b0, b0);
-    x.b1 = min(x.b1, b1);
-    if (x.b0 >= x.b1) x.b0 = x.b1 = 0;
+  auto clip = [](Tile x, int b0, int b1) {  // the tile's steps within blocks [b0, b1)
+    x.s0 = max(x.s0, 2 * b0);
+    x.s1 = min(x.s1, 2 * b1);
+    if (x.s0 >= x.s1) x.s0 = x.s1 = 0;
     return x;
   };
 
   // the blocks that either tile needs: their ranges meet, for a tile's rows
   // follow one another and so do the positions that they see
   auto both = [](const Tile& a, const Tile& b) {
-    if (a.b0 >= a.b1) return make_int2(b.b0, b.b1);
-    if (b.b0 >= b.b1) return make_int2(a.b0, a.b1);
-    return make_int2(min(a.b0, b.b0), max(a.b1, b.b1));
+    if (a.s0 >= a.s1) return make_int2(b.s0 >> 1, (b.s1 + 1) >> 1);
+    if (b.s0 >= b.s1) return make_int2(a.s0 >> 1, (a.s1 + 1) >> 1);
+    return make_int2(min(a.s0, b.s0) >> 1, (max(a.s1, b.s1) + 1) >> 1);
   };
   auto load = [&](int kv0) {
     // ---------------- loads: K and V of each block into the ring, in turn ----------------
@@ -538,12 +555,15 @@ __global__ void __launch_bounds__(Cfg<D, FMT>::THREADS, 1)
   };
   auto multiply = [&](int t) {
     // ---------------- tile t's products, one thread ----------------
-    if (lane == 0) {
-      constexpr uint32_t id_s = idesc(C::kCodes, BK, false), id_o = idesc(C::kCodes, D, true);
+    // S of the next step goes out before the softmax of this one is waited for,
+    // into the other of two buffers: the softmax finds its next scores ready,
+    // and the tensor cores have work whichever tile is slow
+    if (elect_one()) {
+      constexpr uint32_t id_s = idesc(C::kCodes, SK, false), id_o = idesc(C::kCodes, D, true);
       const uint32_t d_s = tmem + t * BK, d_o = tmem + C::T_O + t * D;
       const uint32_t ring_k = desc_k(smem_u32(smem)), ring_v = desc_mn(smem_u32(smem)), q_lo = desc_k(smem_u32(smem) + C::OFF_Q + t * C::SLOT);
-      int slot = 0;
-      uint32_t phase = 0, pph = 0, qph = 0, tph = t ? 0 : 1;  // tile 0 has the first turn
+      int ks = 0, vs = 1;  // slots of the next K and V
+      uint32_t kph = 0, vph = 0, qph = 0, n = 0;  // n: steps so far
       bool dead = dead0;
       auto wait = [&](uint64_t* bar, uint32_t parity) {
         if (!dead && !bar_wait(bar, parity)) {
@@ -551,68 +571,72 @@ __global__ void __launch_bounds__(Cfg<D, FMT>::THREADS, 1)
           dead = true;
         }
       };
-      auto next = [&]() {
-        if (++slot == C::NS) {
-          slot = 0;
-          phase ^= 1;
+      auto advance = [&](int& slot, uint32_t& ph) {
+        umma_commit(&empty[slot]);
+        slot += 2;
+        if (slot >= C::NS) {
+          slot -= C::NS;
+          ph ^= 1;
         }
       };
       walk([&](const SeqRows& s, int, int, const Item& it, long long, int b0, int b1) {
         const Tile t0 = clip(make_tile(s, it, group, window, 0), b0, b1), t1 = clip(make_tile(s, it, group, window, 1), b0, b1);
         const int2 used = both(t0, t1);
-        const int first = t ? t1.b0 : t0.b0, last = t ? t1.b1 : t0.b1;
-        // step j: P of block j - 1 times its V, then S of block j.  The tiles
-        // take turns a step at a time, so that one's products run without a
-        // break while the other's softmax works: left to themselves the two
-        // fall into step, and both wait for products, then both for softmax
-        int vslot = 0;
-        uint32_t vphase = 0;
-        for (int j = used.x; j <= used.y; ++j) {
-          // (a slot is waited for even where the tile skips it: arriving on its
-          // empty barrier a round early would count twice)
-          const bool has_v = j > used.x, has_k = j < used.y;
-          const bool pv = has_v && j > first && j <= last, qk = has_k && j >= first && j < last;
-          if (has_v) wait(&full[vslot], vphase);
-          if (has_k) wait(&full[slot], phase);
-          if (qk && j == first) {
-            wait(&q_full[t], qph);
-            qph ^= 1;
+        const int first = t ? t1.s0 : t0.s0, last = t ? t1.s1 : t0.s1;
+        int kj = used.x, vj = used.x;  // blocks whose K and V are next
+        // a block that only the other tile needs is waited for all the same:
+        // arriving on a slot's empty barrier a round early would count twice
+        auto skip_to = [&](int j) {
+          while (kj < j && !dead) {
+            wait(&full[ks], kph);
+            advance(ks, kph);
+            ++kj;
+            wait(&full[vs], vph);
+            advance(vs, vph);
+            ++vj;
           }
-          wait(&turn[t], tph);
-          tph ^= 1;
-          if (pv) {
-            wait(&p_full[t], pph);
-            pph ^= 1;
-          }
-          if (dead) return false;
+        };
+        auto scores = [&](int i, uint32_t at) {
+          if ((i & 1) == 0 || i == first) wait(&full[ks], kph);
+          if (dead) return;
           tc_fence_after();
-          if (pv) {
-            const uint32_t vb = ring_v + vslot * (C::SLOT >> 4);
-            umma_ts<id_o>(d_o, d_s, vb, j - 1 == first ? 0u : 1u);
+          const uint32_t kb = ring_k + ks * (C::SLOT >> 4) + (i & 1) * (SK * 128 >> 4);
 #pragma unroll
-            for (int k = 1; k < BK / 16; ++k) umma_ts<id_o>(d_o, d_s + k * 8, vb + k * (2048 >> 4), 1u);
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t off = ((k >> 2) * HALF + (k & 3) * 32) >> 4;
+            umma_ss<id_s>(d_s + (at & 1) * SK, q_lo + off, kb + off, k == 0 ? 0u : 1u);
           }
-          if (qk) {
-            const uint32_t kb = ring_k + slot * (C::SLOT >> 4);
+          umma_commit(&s_full[2 * t + (at & 1)]);
+          if ((i & 1) || i + 1 == last) {
+            advance(ks, kph);
+            ++kj;
+          }
+        };
+        if (first < last) {
+          skip_to(first >> 1);
+          wait(&q_full[t], qph);
+          qph ^= 1;
+          scores(first, n);
+          for (int i = first; i < last && !dead; ++i, ++n) {
+            if (i + 1 < last) scores(i + 1, n + 1);
+            if ((i & 1) == 0 || i == first) wait(&full[vs], vph);
+            wait(&p_full[2 * t + (n & 1)], (n >> 1) & 1);
+            if (dead) return false;
+            tc_fence_after();
+            const uint32_t vb = ring_v + vs * (C::SLOT >> 4) + (i & 1) * (SK * 128 >> 4), pb = d_s + (n & 1) * SK;
+            umma_ts<id_o>(d_o, pb, vb, i == first ? 0u : 1u);
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-              const uint32_t off = ((k >> 2) * HALF + (k & 3) * 32) >> 4;
-              umma_ss<id_s>(d_s, q_lo + off, kb + off, k == 0 ? 0u : 1u);
+            for (int k = 1; k < SK / 16; ++k) umma_ts<id_o>(d_o, pb + k * 8, vb + k * (2048 >> 4), 1u);
+            umma_commit(&v_done[t]);
+            if (i + 1 == last) umma_commit(&o_full[t]);
+            if ((i & 1) || i + 1 == last) {
+              advance(vs, vph);
+              ++vj;
             }
-            umma_commit(&s_full[t]);
-          }
-          mbar_arrive(&turn[1 - t]);
-          if (pv && j == last) umma_commit(&o_full[t]);
-          if (has_v) umma_commit(&empty[vslot]);
-          if (has_k) {
-            umma_commit(&empty[slot]);
-            next();
-            vslot = slot;
-            vphase = phase;
-            next();
           }
         }
-        return true;
+        skip_to(used.y);
+        return !dead;
       });
       // every product has ended before the block gives its TMEM back
       umma_commit(done);
@@ -625,7 +649,7 @@ __global__ void __launch_bounds__(Cfg<D, FMT>::THREADS, 1)
     const int t = warp >> 2, i = tid & (BM - 1);
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t t_s = tmem + lanes + t * BK, t_o = tmem + lanes + C::T_O + t * D;
-    uint32_t sph = 0, oph = 0;
+    uint32_t n = 0, oph = 0;  // n: steps so far
     bool dead = dead0;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       if (!dead && !bar_wait(bar, parity)) {
@@ -643,7 +667,7 @@ __global__ void __launch_bounds__(Cfg<D, FMT>::THREADS, 1)
       const long long tok = s.off + (in ? row / group : 0);
       const int head = h * group + (in ? row % group : 0);
       float cz = p.scale_log2, m = kNoMax, l = 0.f;
-      if (x.b0 < x.b1 && !dead) {
+      if (x.s0 < x.s1 && !dead) {
         // this row's query into the tile (its last reader, the item before, is done: its scores were all read)
         const uint4* src = reinterpret_cast<const uint4*>(p.q + tok * p.q_stride + (long long)head * D);
         uint8_t* dst = smem + C::OFF_Q + t * C::SLOT + i * 128;
@@ -678,12 +702,12 @@ __global__ void __launch_bounds__(Cfg<D, FMT>::THREADS, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&q_full[t]);
       }
-      for (int j = x.b0; j < x.b1; ++j) {
-        wait(&s_full[t], sph);
-        sph ^= 1;
+      for (int j = x.s0; j < x.s1; ++j, ++n) {
+        wait(&s_full[2 * t + (n & 1)], (n >> 1) & 1);
         if (dead) break;
-        const int key0 = it.page_lo * kPage + j * BK;
-        const bool full_block = key0 + BK - 1 <= x.pmin && (window <= 0 || key0 > x.pmax - window);
+        const uint32_t t_sb = t_s + (n & 1) * SK;
+        const int key0 = it.page_lo * kPage + j * SK;
+        const bool full_block = key0 + SK - 1 <= x.pmin && (window <= 0 || key0 > x.pmax - window);
         const int rel = pos - key0;  // key column c is seen when c <= rel and c > rel - window
         const int low = window > 0 ? rel - window : -0x40000000;
         uint32_t buf[2][32];
@@ -697,8 +721,8 @@ __global__ void __launch_bounds__(Cfg<D, FMT>::THREADS, 1)
         auto row_top = [&]() {  // the block's largest logit
           float v = -INFINITY;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            tmem_ld32(t_s + 32 * c, buf[0]);
+          for (int c = 0; c < SK / 32; ++c) {
+            tmem_ld32(t_sb + 32 * c, buf[0]);
             tmem_wait_ld(buf[0]);
             mask(buf[0], 32 * c);
 #pragma unroll
@@ -706,16 +730,16 @@ __global__ void __launch_bounds__(Cfg<D, FMT>::THREADS, 1)
           }
           return v * cz;
         };
-        if (j == x.b0) m = fmaxf(kNoMax, row_top());  // the first block sets the bound
-        uint32_t pw[2][32];
+        if (j == x.s0) m = fmaxf(kNoMax, row_top());  // the first step sets the bound
+        uint32_t pw[SK / 2];
         for (int again = 0;; ++again) {
           uint64_t sum[2] = {0, 0};
           const uint64_t cc = f2(cz, cz), mm = f2(-m, -m);
-          tmem_ld32(t_s, buf[0]);
+          tmem_ld32(t_sb, buf[0]);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
+          for (int c = 0; c < SK / 32; ++c) {
             tmem_wait_ld(buf[c & 1]);
-            if (c < 3) tmem_ld32(t_s + 32 * (c + 1), buf[(c + 1) & 1]);
+            if (c + 1 < SK / 32) tmem_ld32(t_sb + 32 * (c + 1), buf[(c + 1) & 1]);
             uint32_t (&r)[32] = buf[c & 1];
             mask(r, 32 * c);
 #pragma unroll
@@ -727,9 +751,9 @@ __global__ void __launch_bounds__(Cfg<D, FMT>::THREADS, 1)
               sum[(k >> 1) & 1] = add2(sum[(k >> 1) & 1], f2(a, b));
               if constexpr (C::kCodes) {
                 const __half2 y = __floats2half2_rn(a, b);
-                pw[c >> 1][(c & 1) * 16 + (k >> 1)] = *reinterpret_cast<const uint32_t*>(&y);
+                pw[c * 16 + (k >> 1)] = *reinterpret_cast<const uint32_t*>(&y);
               } else {
-                pw[c >> 1][(c & 1) * 16 + (k >> 1)] = pack_bf16x2(a, b);
+                pw[c * 16 + (k >> 1)] = pack_bf16x2(a, b);
               }
             }
           }
@@ -745,7 +769,9 @@ __global__ void __launch_bounds__(Cfg<D, FMT>::THREADS, 1)
           const float mn = fmaxf(m, row_top()), f = fast_ex2(m - mn);
           m = mn;
           l *= f;
-          if (j > x.b0) {
+          if (j > x.s0) {
+            // the step before has been added (all before it had when these scores were made)
+            wait(&v_done[t], (n - 1) & 1);
             const uint64_t ff = f2(f, f);
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
@@ -763,14 +789,13 @@ __global__ void __launch_bounds__(Cfg<D, FMT>::THREADS, 1)
             tmem_wait_st();
           }
         }
-        tmem_st32(t_s, pw[0]);
-        tmem_st32(t_s + 32, pw[1]);
+        tmem_st32(t_sb, pw);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[t]);
+        if (lane == 0) mbar_arrive(&p_full[2 * t + (n & 1)]);
       }
-      if (x.b0 < x.b1) {
+      if (x.s0 < x.s1) {
         wait(&o_full[t], oph);
         oph ^= 1;
       }
@@ -782,7 +807,7 @@ __global__ void __launch_bounds__(Cfg<D, FMT>::THREADS, 1)
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
           uint32_t r[32];
-          if (x.b0 < x.b1 && !dead) {
+          if (x.s0 < x.s1 && !dead) {
             tmem_ld32(t_o + 32 * c, r);
             tmem_wait_ld(r);
           } else {
@@ -806,7 +831,7 @@ __global__ void __launch_bounds__(Cfg<D, FMT>::THREADS, 1)
       constexpr long long PF = (long long)BM * (D + 2);
       auto part_of = [&](int cta) { return p.part + ((2LL * cta + (cta == c_first)) * 2 + t) * PF; };
       float* mine = part_of(blockIdx.x);
-      if (x.b0 < x.b1 && !dead) {
+      if (x.s0 < x.s1 && !dead) {
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
           uint32_t r[32];
