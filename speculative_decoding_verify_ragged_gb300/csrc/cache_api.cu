@@ -8,7 +8,7 @@
 
 struct sdv_cache {
   sdv_cache_config cfg;
-  int device, sms, max_rows, max_slots, grid;
+  int device, sms, max_rows, max_slots;
   float *part, *part_tc;
   int *counters, *counters_tc;
   sdv::RopeTurns turns;
@@ -38,15 +38,13 @@ constexpr int kSmallRows = 16;
 
 struct Space {
   size_t counters, counters_tc, part, part_tc, total;
-  int grid;
 };
 Space space(const sdv_cache_config& c, int sms) {
   Space s{};
-  s.grid = chunk_attn_grid(c.head_dim, c.cache_format, sms);
   s.counters = 0;
-  s.counters_tc = up256(s.grid * sizeof(int));
+  s.counters_tc = up256(chunk_attn_grid_max(sms) * sizeof(int));
   s.part = s.counters_tc + up256(2 * sms * sizeof(int));
-  s.part_tc = s.part + up256(static_cast<size_t>(2) * s.grid * 16 * (c.head_dim + 2) * sizeof(float));
+  s.part_tc = s.part + up256(chunk_attn_part_floats(c.head_dim, sms) * sizeof(float));
   s.total = s.part_tc + up256(chunk_attn_tc_part_floats(c.head_dim, sms) * sizeof(float));
   return s;
 }
@@ -125,7 +123,6 @@ extern "C" sdv_status sdv_cache_create(const sdv_cache_config* cfg, void* worksp
   h->sms = sms;
   h->max_rows = max_rows;
   h->max_slots = max_slots;
-  h->grid = s.grid;
   h->counters = reinterpret_cast<int*>(static_cast<uint8_t*>(workspace) + s.counters);
   h->counters_tc = reinterpret_cast<int*>(static_cast<uint8_t*>(workspace) + s.counters_tc);
   h->part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + s.part);
@@ -194,7 +191,8 @@ extern "C" sdv_status sdv_cache_attention(sdv_cache* h, const sdv_chunk* chunk, 
   p.scale_log2 = kLog2e / std::sqrt(static_cast<float>(d));
   p.small_rows = 0x7FFFFFFF;
   const int group = h->cfg.n_q / h->cfg.n_kv;
-  if ((long long)(chunk->max_q < chunk->T ? chunk->max_q : chunk->T) * group > kSmallRows) {
+  const long long rows = (long long)(chunk->max_q < chunk->T ? chunk->max_q : chunk->T) * group;  // of a sequence at most
+  if (rows > kSmallRows) {
     p.small_rows = kSmallRows;
     p.part = h->part_tc;
     p.counters = h->counters_tc;
@@ -209,7 +207,7 @@ extern "C" sdv_status sdv_cache_attention(sdv_cache* h, const sdv_chunk* chunk, 
   }
   p.part = h->part;
   p.counters = h->counters;
-  return launched(launch_chunk_attn(d, h->cfg.cache_format, p, h->grid, static_cast<cudaStream_t>(stream)));
+  return launched(launch_chunk_attn(d, h->cfg.cache_format, rows <= 8, p, h->sms, static_cast<cudaStream_t>(stream)));
 }
 
 extern "C" sdv_status sdv_cache_read(sdv_cache* h, const sdv_chunk* chunk, void* k_out, long long k_stride, void* v_out,

@@ -130,10 +130,13 @@ size_t chunk_attn_tc_part_floats(int head_dim, int grid);
 cudaError_t setup_chunk_attn_tc(int head_dim, int cache_format);
 cudaError_t launch_chunk_attn_tc(int head_dim, int cache_format, const CUtensorMap& map, const ChunkAttnParams& p, int grid,
                                  cudaStream_t stream);
-// Blocks a launch of the mma.sync kernel uses at most (its partials and counters are sized by it).
-int chunk_attn_grid(int head_dim, int cache_format, int sms);
+// Sequences of few rows on mma.sync, in items of 8 (eight) or 16 packed rows
+// (chunk_attention.cu); chunk_attn_grid_max: blocks of a launch at most.
+constexpr int kItemRows = 16;
+int chunk_attn_grid_max(int sms);
+size_t chunk_attn_part_floats(int head_dim, int sms);
 // Once per device before the first launch.
 cudaError_t setup_chunk_attn(int head_dim, int cache_format);
-cudaError_t launch_chunk_attn(int head_dim, int cache_format, const ChunkAttnParams& p, int grid, cudaStream_t stream);
+cudaError_t launch_chunk_attn(int head_dim, int cache_format, bool eight, const ChunkAttnParams& p, int sms, cudaStream_t stream);
 
 }  // namespace sdv

@@ -1,20 +1,21 @@
 // Attention of a ragged chunk over the paged cache, for few query rows per
 // sequence (mma.sync): softmax(q k^T / sqrt(d)) v with a running maximum and sum.
 //
-// An item is 16 packed query rows -- the n_q / n_kv heads of consecutive tokens
-// -- of one (sequence, key head) against its visible pages.  The items' pages
-// are laid end to end and cut into equal runs, one per block, so a single
+// An item is 8 or 16 packed query rows -- the n_q / n_kv heads of consecutive
+// tokens -- of one (sequence, key head) against its visible pages.  The items'
+// pages are laid end to end and cut into equal runs, one per block, so a single
 // long sequence and a batch of unlike ones load the GPU alike; an item cut
 // between blocks is joined by the last of them to arrive, in block order, so
 // equal inputs give equal bits.
 //
 // Within a block the four warps take pages in turn, straight from global memory
-// to registers: the sum over d of a score may run in any order, so a lane takes
-// 16 contiguous bytes of a key wherever the MMA wants its k index, and queries
-// are laid out to match; the columns of the output are likewise assigned so
-// that a lane's V loads are 16 contiguous bytes of four keys.  No value is
-// staged in shared memory.  e4m3 codes become fp16 exactly; a key's scale
-// multiplies its scores, a value's its weight.
+// to registers.  Scores and output are computed transposed (16 keys, or 16
+// columns, by 8 rows), so that 8 rows fill the MMA.  The sum over d of a
+// score may run in any order, so a lane takes 16 contiguous bytes of a key
+// wherever the MMA wants its k index, and queries are laid out to match; the
+// columns of the output are likewise assigned so that a lane's V loads are 16
+// contiguous bytes of four keys.  No value is staged in shared memory.  e4m3 codes
+// become fp16 exactly; a key's scale multiplies its scores, a value's its weight.
 #include "chunk.cuh"
 
 namespace sdv {
@@ -22,12 +23,11 @@ namespace {
 
 constexpr int CA_WARPS = 4;
 constexpr int CA_THREADS = CA_WARPS * kWarp;
-constexpr int ROWS = 16;          // packed query rows of an item
 constexpr float kNoMax = -1e30f;  // the maximum before the first visible key
 constexpr int kMinPages = 4;      // pages a block takes at least: one per warp
 constexpr int kSplitBias = 8;     // e4m3: weights carry 2^(e + 8), in fp16's normal range for every e
 
-constexpr int part_floats(int D) { return ROWS * (D + 2); }
+constexpr int part_floats(int D) { return kItemRows * (D + 2); }
 
 template <int D, int FMT>
 struct Frag {
@@ -36,17 +36,25 @@ struct Frag {
   static constexpr int ROW_BYTES = kCodes ? D : 2 * D;
   static constexpr int KCH = ROW_BYTES / 64;                    // 16-byte chunks of a key row per lane (4 lanes a row)
   static constexpr int VW = ROW_BYTES / 8 / 4;                  // words of a value row per lane (8 lanes a row)
-  static constexpr int NT = D / 8;                              // 8-column tiles of the output
+  static constexpr int MT = D / 16;                             // 16-row tiles of the transposed output
   uint32_t k[2][KCH * 4];  // keys g and g + 8
   uint32_t v[4][VW];       // keys 2t, 2t + 1, 2t + 8, 2t + 9
-  uint32_t sc[2];          // e4m3: scale bytes of keys (2t, 2t + 1) and of (2t + 8, 2t + 9): K low half, V high half
+  uint32_t sc[2];          // e4m3: scale bytes of keys g and g + 8: K's low byte, V's above
 };
 
-// The output column of (lane group g of 8, tile j): the V words of a lane are contiguous.
+// The output column of (lane group g of 8, tile j), its neighbour following in
+// the tile's rows g + 8: the V words of a lane are contiguous.
 template <int D, int FMT>
 __device__ __forceinline__ int out_col(int g, int j) {
-  if constexpr (FMT == SDV_CACHE_E4M3) return g * (D / 8) + j;
-  return ((j >> 3) * 8 + g) * 8 + (j & 7);
+  if constexpr (FMT == SDV_CACHE_E4M3) return g * (D / 8) + 2 * j;
+  return ((j >> 2) * 8 + g) * 8 + 2 * (j & 3);
+}
+
+// Transpose of an 8 x 8 matrix of 16-bit values, one row of pairs per four lanes.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
 }
 
 // Cache loads are used once by this SM: kept out of L1.
@@ -93,15 +101,20 @@ __device__ __forceinline__ void load_page(Frag<D, FMT>& f, const ChunkParams& c,
   if constexpr (F::kCodes) {
     const uint8_t* s = c.scales + head;
 #pragma unroll
-    for (int r = 0; r < 2; ++r)
-      f.sc[r] = static_cast<uint32_t>(*reinterpret_cast<const unsigned short*>(s + 2 * t + 8 * r)) |
-                static_cast<uint32_t>(*reinterpret_cast<const unsigned short*>(s + kPage + 2 * t + 8 * r)) << 16;
+    for (int r = 0; r < 2; ++r) f.sc[r] = static_cast<uint32_t>(s[g + 8 * r]) | static_cast<uint32_t>(s[kPage + g + 8 * r]) << 8;
   }
 }
 
-template <int D, int FMT>
-__global__ void __launch_bounds__(CA_THREADS, 2) chunk_attn_kernel(const ChunkAttnParams p) {
+// Blocks per SM: what the registers allow (held: two pages, the output, the queries).
+template <int D, int FMT, int NT>
+constexpr int per_sm() {
+  return D == 64 ? 4 : FMT == SDV_CACHE_E4M3 ? (NT == 1 ? 3 : 2) : 2;
+}
+
+template <int D, int FMT, int NT>
+__global__ void __launch_bounds__(CA_THREADS, per_sm<D, FMT, NT>()) chunk_attn_kernel(const ChunkAttnParams p) {
   using F = Frag<D, FMT>;
+  constexpr int ROWS = 8 * NT;
   extern __shared__ __align__(16) uint8_t smem_raw[];
   float* s_o = reinterpret_cast<float*>(smem_raw);                     // [warps][16][D]
   float* s_ml = s_o + CA_WARPS * ROWS * D;                             // [warps][2][16]
@@ -183,18 +196,18 @@ __global__ void __launch_bounds__(CA_THREADS, 2) chunk_attn_kernel(const ChunkAt
     const int first = max(lo_page + page0, window > 0 ? max(0, pmin - window + 1) / kPage : 0);
     const int last = min(lo_page + page0 + n_here, pmax < 0 ? 0 : pmax / kPage + 1);
 
-    // queries: rows g and g + 8, laid out like the keys
-    uint32_t qf[F::KSTEPS][4];
-    int pos[2];
-    float cz[2];
+    // queries: row g of each 8, laid out like the keys; the rows whose scores
+    // this lane holds are 2 t and 2 t + 1 of each 8
+    uint32_t qf[NT][F::KSTEPS][2];
+    int pos[NT][2];
+    float cz[NT][2];
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
+    for (int r = 0; r < NT; ++r) {
       const int row = row0 + g + 8 * r;
       const bool in = g + 8 * r < n_rows;
-      pos[r] = in ? sq.pos0 + row / group : -1;
       const __nv_bfloat16* src =
           p.q + (in ? (long long)(sq.off + row / group) * p.q_stride + (long long)(h * group + row % group) * D : 0);
-      cz[r] = p.scale_log2;
+      float scale = p.scale_log2;
       if constexpr (F::kCodes) {
         // fp16 with the row's largest magnitude in [1/2, 1): what falls below
         // 2^-25 of it is lost, far under the products' own rounding
@@ -210,27 +223,39 @@ __global__ void __launch_bounds__(CA_THREADS, 2) chunk_attn_kernel(const ChunkAt
         a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
         const int e = min(max(static_cast<int>(__float_as_uint(a) >> 23) - 126, -100), 100);
         const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-        cz[r] *= __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+        scale *= __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
 #pragma unroll
         for (int ks = 0; ks < F::KSTEPS; ++ks) {
           const __half2 x = __floats2half2_rn(__uint_as_float(w[ks].x << 16) * inv, __uint_as_float(w[ks].x & 0xFFFF0000u) * inv);
           const __half2 y = __floats2half2_rn(__uint_as_float(w[ks].y << 16) * inv, __uint_as_float(w[ks].y & 0xFFFF0000u) * inv);
-          qf[ks][r] = *reinterpret_cast<const uint32_t*>(&x);
-          qf[ks][2 + r] = *reinterpret_cast<const uint32_t*>(&y);
+          qf[r][ks][0] = *reinterpret_cast<const uint32_t*>(&x);
+          qf[r][ks][1] = *reinterpret_cast<const uint32_t*>(&y);
         }
       } else {
 #pragma unroll
         for (int i = 0; i < F::KCH; ++i) {
           const uint4 w = in ? *reinterpret_cast<const uint4*>(src + (i * 4 + t) * 8) : make_uint4(0u, 0u, 0u, 0u);
-          qf[2 * i][r] = w.x, qf[2 * i][2 + r] = w.y, qf[2 * i + 1][r] = w.z, qf[2 * i + 1][2 + r] = w.w;
+          qf[r][2 * i][0] = w.x, qf[r][2 * i][1] = w.y, qf[r][2 * i + 1][0] = w.z, qf[r][2 * i + 1][1] = w.w;
         }
+      }
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int rr = 2 * t + x + 8 * r;
+        pos[r][x] = rr < n_rows ? sq.pos0 + (row0 + rr) / group : -1;
+        cz[r][x] = __shfl_sync(0xffffffffu, scale, (2 * t + x) * 4);
       }
     }
 
-    float o[F::NT][4];
+    // the output transposed: o[r][j] holds columns out_col(g, j) and the next of rows 2 t and 2 t + 1
+    float o[NT][F::MT][4];
+    float m[NT][2], l[NT][2];
 #pragma unroll
-    for (int j = 0; j < F::NT; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
-    float m[2] = {kNoMax, kNoMax}, l[2] = {0.f, 0.f};
+    for (int r = 0; r < NT; ++r) {
+#pragma unroll
+      for (int j = 0; j < F::MT; ++j) o[r][j][0] = o[r][j][1] = o[r][j][2] = o[r][j][3] = 0.f;
+      m[r][0] = m[r][1] = kNoMax;
+      l[r][0] = l[r][1] = 0.f;
+    }
 
     const int pg0 = first + warp;
     const int mine = dead || pg0 >= last ? 0 : (last - pg0 + CA_WARPS - 1) / CA_WARPS;  // this warp's pages
@@ -254,121 +279,139 @@ __global__ void __launch_bounds__(CA_THREADS, 2) chunk_attn_kernel(const ChunkAt
       cur = nxt;
       if (i + 1 < mine) load_page(nxt, p.c, page_id(i + 1), h, g, t);
       const int key0 = (pg0 + i * CA_WARPS) * kPage;
-      float s[2][4];
+      // scores transposed: s[r][2 y + x] is key key0 + g + 8 y, row 2 t + x of 8-row tile r
+      float s[NT][4];
 #pragma unroll
-      for (int n = 0; n < 2; ++n) {
-        s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+      for (int r = 0; r < NT; ++r) s[r][0] = s[r][1] = s[r][2] = s[r][3] = 0.f;
 #pragma unroll
-        for (int ks = 0; ks < F::KSTEPS; ++ks) {
-          if constexpr (F::kCodes) {
-            const uint32_t w = cur.k[n][ks];
-            mma_f16(s[n], qf[ks], e4m3x2_to_f16x2(w & 0xFFFFu), e4m3x2_to_f16x2(w >> 16));
-          } else {
-            mma_bf16(s[n], qf[ks], cur.k[n][2 * ks], cur.k[n][2 * ks + 1]);
-          }
+      for (int ks = 0; ks < F::KSTEPS; ++ks) {
+        uint32_t a[4];
+        if constexpr (F::kCodes) {
+          a[0] = e4m3x2_to_f16x2(cur.k[0][ks] & 0xFFFFu), a[1] = e4m3x2_to_f16x2(cur.k[1][ks] & 0xFFFFu);
+          a[2] = e4m3x2_to_f16x2(cur.k[0][ks] >> 16), a[3] = e4m3x2_to_f16x2(cur.k[1][ks] >> 16);
+#pragma unroll
+          for (int r = 0; r < NT; ++r) mma_f16(s[r], a, qf[r][ks][0], qf[r][ks][1]);
+        } else {
+          a[0] = cur.k[0][2 * ks], a[1] = cur.k[1][2 * ks], a[2] = cur.k[0][2 * ks + 1], a[3] = cur.k[1][2 * ks + 1];
+#pragma unroll
+          for (int r = 0; r < NT; ++r) mma_bf16(s[r], a, qf[r][ks][0], qf[r][ks][1]);
         }
       }
-      // base-2 logits; s[n][2 r + c] is row g + 8 r, key key0 + 8 n + 2 t + c
-      float vs[2][2];
+      // base-2 logits
+      float vs[2] = {1.f, 1.f};
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
-#pragma unroll
-        for (int cc = 0; cc < 2; ++cc) {
-          float ksc = 1.f;
-          vs[n][cc] = 1.f;
-          if constexpr (F::kCodes) {
-            ksc = scale_value(cur.sc[n] >> (8 * cc));
-            vs[n][cc] = scale_value((cur.sc[n] >> (16 + 8 * cc)) + kSplitBias);
-          }
-          s[n][cc] *= cz[0] * ksc;
-          s[n][2 + cc] *= cz[1] * ksc;
+      for (int y = 0; y < 2; ++y) {
+        float ksc = 1.f;
+        if constexpr (F::kCodes) {
+          ksc = scale_value(cur.sc[y]);
+          vs[y] = scale_value((cur.sc[y] >> 8) + kSplitBias);
         }
+#pragma unroll
+        for (int r = 0; r < NT; ++r) {
+          s[r][2 * y] *= cz[r][0] * ksc;
+          s[r][2 * y + 1] *= cz[r][1] * ksc;
+        }
+      }
       const bool full = key0 + kPage - 1 <= pmin && (window <= 0 || key0 > pmax - window);
       if (!full) {
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const int key = key0 + 8 * n + 2 * t + (x & 1), ps = pos[x >> 1];
-            if (key > ps || (window > 0 && key <= ps - window)) s[n][x] = -INFINITY;
-          }
         // keys that no row of the item sees may hold anything: their weight is
         // 0 and their values are taken as 0
 #pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const int key = key0 + g + 8 * y;
+          if (key > pmax || (window > 0 && key <= pmin - window)) vs[y] = 0.f;
+#pragma unroll
+          for (int r = 0; r < NT; ++r)
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+              if (key > pos[r][x] || (window > 0 && key <= pos[r][x] - window)) s[r][2 * y + x] = -INFINITY;
+        }
+#pragma unroll
         for (int r = 0; r < 4; ++r) {
           const int key = key0 + 2 * t + (r & 1) + 8 * (r >> 1);
-          if (key > pmax || (window > 0 && key <= pmin - window)) {
-            vs[r >> 1][r & 1] = 0.f;
+          if (key > pmax || (window > 0 && key <= pmin - window))
 #pragma unroll
             for (int w = 0; w < F::VW; ++w) cur.v[r][w] = 0u;
+        }
+      }
+      bool up = false;
+#pragma unroll
+      for (int r = 0; r < NT; ++r) up |= fmaxf(s[r][0], s[r][2]) > m[r][0] || fmaxf(s[r][1], s[r][3]) > m[r][1];
+      if (__any_sync(0xffffffffu, up)) {
+#pragma unroll
+        for (int r = 0; r < NT; ++r)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            float top = fmaxf(fmaxf(s[r][x], s[r][2 + x]), m[r][x]);
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+            const float f = fast_ex2(m[r][x] - top);
+            m[r][x] = top;
+            l[r][x] *= f;
+#pragma unroll
+            for (int j = 0; j < F::MT; ++j) o[r][j][x] *= f, o[r][j][2 + x] *= f;
           }
-        }
       }
-      float top[2];
+      uint32_t pb[NT][2];
 #pragma unroll
-      for (int r = 0; r < 2; ++r) top[r] = fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]), fmaxf(s[1][2 * r], s[1][2 * r + 1]));
-      if (__any_sync(0xffffffffu, top[0] > m[0] || top[1] > m[1])) {
+      for (int r = 0; r < NT; ++r)
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          float x = fmaxf(top[r], m[r]);
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-          const float a = fast_ex2(m[r] - x);
-          m[r] = x;
-          l[r] *= a;
-#pragma unroll
-          for (int j = 0; j < F::NT; ++j) o[j][2 * r] *= a, o[j][2 * r + 1] *= a;
-        }
-      }
-      uint32_t pa[4];
-#pragma unroll
-      for (int n = 0; n < 2; ++n)
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const float x = fast_ex2(s[n][2 * r] - m[r]), y = fast_ex2(s[n][2 * r + 1] - m[r]);
-          l[r] += x + y;
+        for (int y = 0; y < 2; ++y) {
+          const float a = fast_ex2(s[r][2 * y] - m[r][0]), b2 = fast_ex2(s[r][2 * y + 1] - m[r][1]);
+          l[r][0] += a;
+          l[r][1] += b2;
+          uint32_t w;
           if constexpr (F::kCodes) {
-            const __half2 w = __floats2half2_rn(x * vs[n][0], y * vs[n][1]);
-            pa[2 * n + r] = *reinterpret_cast<const uint32_t*>(&w);
+            const __half2 hw = __floats2half2_rn(a * vs[y], b2 * vs[y]);
+            w = *reinterpret_cast<const uint32_t*>(&hw);
           } else {
-            pa[2 * n + r] = pack_bf16x2(x, y);
+            w = pack_bf16x2(a, b2);
           }
+          pb[r][y] = transpose8(w);
         }
 #pragma unroll
       for (int w = 0; w < F::VW; ++w) {
+        uint32_t a[4];
         if constexpr (F::kCodes) {
-          const uint32_t a0 = __byte_perm(cur.v[0][w], cur.v[1][w], 0x5140), a1 = __byte_perm(cur.v[0][w], cur.v[1][w], 0x7362);
-          const uint32_t b0 = __byte_perm(cur.v[2][w], cur.v[3][w], 0x5140), b1 = __byte_perm(cur.v[2][w], cur.v[3][w], 0x7362);
-          mma_f16(o[4 * w], pa, e4m3x2_to_f16x2(a0 & 0xFFFFu), e4m3x2_to_f16x2(b0 & 0xFFFFu));
-          mma_f16(o[4 * w + 1], pa, e4m3x2_to_f16x2(a0 >> 16), e4m3x2_to_f16x2(b0 >> 16));
-          mma_f16(o[4 * w + 2], pa, e4m3x2_to_f16x2(a1 & 0xFFFFu), e4m3x2_to_f16x2(b1 & 0xFFFFu));
-          mma_f16(o[4 * w + 3], pa, e4m3x2_to_f16x2(a1 >> 16), e4m3x2_to_f16x2(b1 >> 16));
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const uint32_t lo = __byte_perm(cur.v[0][w], cur.v[1][w], y ? 0x7362 : 0x5140);
+            const uint32_t hi = __byte_perm(cur.v[2][w], cur.v[3][w], y ? 0x7362 : 0x5140);
+            a[0] = e4m3x2_to_f16x2(lo & 0xFFFFu), a[1] = e4m3x2_to_f16x2(lo >> 16);
+            a[2] = e4m3x2_to_f16x2(hi & 0xFFFFu), a[3] = e4m3x2_to_f16x2(hi >> 16);
+#pragma unroll
+            for (int r = 0; r < NT; ++r) mma_f16(o[r][2 * w + y], a, pb[r][0], pb[r][1]);
+          }
         } else {
-          mma_bf16(o[2 * w], pa, __byte_perm(cur.v[0][w], cur.v[1][w], 0x5410), __byte_perm(cur.v[2][w], cur.v[3][w], 0x5410));
-          mma_bf16(o[2 * w + 1], pa, __byte_perm(cur.v[0][w], cur.v[1][w], 0x7632), __byte_perm(cur.v[2][w], cur.v[3][w], 0x7632));
+          a[0] = __byte_perm(cur.v[0][w], cur.v[1][w], 0x5410), a[1] = __byte_perm(cur.v[0][w], cur.v[1][w], 0x7632);
+          a[2] = __byte_perm(cur.v[2][w], cur.v[3][w], 0x5410), a[3] = __byte_perm(cur.v[2][w], cur.v[3][w], 0x7632);
+#pragma unroll
+          for (int r = 0; r < NT; ++r) mma_bf16(o[r][w], a, pb[r][0], pb[r][1]);
         }
       }
     }
 
-    // the warps' parts into shared memory, then joined: 8 threads a row
+    // the warps' parts into shared memory, then joined
     const float undo = F::kCodes ? 1.f / (1 << kSplitBias) : 1.f;
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-      if (t == 0) {
-        s_ml[warp * 2 * ROWS + g + 8 * r] = m[r];
-        s_ml[warp * 2 * ROWS + ROWS + g + 8 * r] = l[r];
-      }
+    for (int r = 0; r < NT; ++r)
 #pragma unroll
-      for (int j = 0; j < F::NT; ++j) {
-        s_o[(warp * ROWS + g + 8 * r) * D + out_col<D, FMT>(2 * t, j)] = o[j][2 * r] * undo;
-        s_o[(warp * ROWS + g + 8 * r) * D + out_col<D, FMT>(2 * t + 1, j)] = o[j][2 * r + 1] * undo;
+      for (int x = 0; x < 2; ++x) {
+        const int row = 8 * r + 2 * t + x;
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) l[r][x] += __shfl_xor_sync(0xffffffffu, l[r][x], d);
+        if (g == 0) {
+          s_ml[warp * 2 * ROWS + row] = m[r][x];
+          s_ml[warp * 2 * ROWS + ROWS + row] = l[r][x];
+        }
+#pragma unroll
+        for (int j = 0; j < F::MT; ++j)
+          *reinterpret_cast<float2*>(s_o + (warp * ROWS + row) * D + out_col<D, FMT>(g, j)) =
+              make_float2(o[r][j][x] * undo, o[r][j][2 + x] * undo);
       }
-    }
     __syncthreads();
-    constexpr int PER = D / 8;
-    const int row = tid >> 3, c0 = (tid & 7) * PER;
+    constexpr int TPR = CA_THREADS / ROWS, PER = D / TPR;  // threads a row, columns a thread
+    const int row = tid / TPR, c0 = (tid % TPR) * PER;
     float acc[PER], M = kNoMax, L = 0.f;
 #pragma unroll
     for (int j = 0; j < PER; ++j) acc[j] = 0.f;
@@ -393,9 +436,9 @@ __global__ void __launch_bounds__(CA_THREADS, 2) chunk_attn_kernel(const ChunkAt
 #pragma unroll
       for (int j = 0; j < PER; j += 4)
         *reinterpret_cast<float4*>(mine_part + row * D + c0 + j) = make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
-      if ((tid & 7) == 0) {
-        mine_part[ROWS * D + row] = M;
-        mine_part[ROWS * D + ROWS + row] = L;
+      if (tid % TPR == 0) {
+        mine_part[kItemRows * D + row] = M;
+        mine_part[kItemRows * (D + 1) + row] = L;
       }
       __threadfence();
       __syncthreads();
@@ -409,14 +452,14 @@ __global__ void __launch_bounds__(CA_THREADS, 2) chunk_attn_kernel(const ChunkAt
       if (s_last) {
         M = kNoMax;
         for (int cta = c_first; cta <= c_last; ++cta)
-          M = fmaxf(M, __ldcg(p.part + (2LL * cta + (cta == c_first)) * PF + ROWS * D + row));
+          M = fmaxf(M, __ldcg(p.part + (2LL * cta + (cta == c_first)) * PF + kItemRows * D + row));
         L = 0.f;
 #pragma unroll
         for (int j = 0; j < PER; ++j) acc[j] = 0.f;
         for (int cta = c_first; cta <= c_last; ++cta) {
           const float* src = p.part + (2LL * cta + (cta == c_first)) * PF;
-          const float a = fast_ex2(__ldcg(src + ROWS * D + row) - M);
-          L += a * __ldcg(src + ROWS * D + ROWS + row);
+          const float a = fast_ex2(__ldcg(src + kItemRows * D + row) - M);
+          L += a * __ldcg(src + kItemRows * (D + 1) + row);
 #pragma unroll
           for (int j = 0; j < PER; j += 4) {
             const float4 x = __ldcg(reinterpret_cast<const float4*>(src + row * D + c0 + j));
@@ -430,32 +473,37 @@ __global__ void __launch_bounds__(CA_THREADS, 2) chunk_attn_kernel(const ChunkAt
       const int rr = row0 + row;
       __nv_bfloat16* dst = p.out + (long long)(sq.off + rr / group) * p.out_stride + (long long)(h * group + rr % group) * D + c0;
 #pragma unroll
-      for (int j = 0; j < PER; j += 8)
-        *reinterpret_cast<uint4*>(dst + j) =
-            make_uint4(pack_bf16x2(acc[j] * inv, acc[j + 1] * inv), pack_bf16x2(acc[j + 2] * inv, acc[j + 3] * inv),
-                       pack_bf16x2(acc[j + 4] * inv, acc[j + 5] * inv), pack_bf16x2(acc[j + 6] * inv, acc[j + 7] * inv));
+      for (int j = 0; j < PER; j += 4)
+        *reinterpret_cast<uint2*>(dst + j) =
+            make_uint2(pack_bf16x2(acc[j] * inv, acc[j + 1] * inv), pack_bf16x2(acc[j + 2] * inv, acc[j + 3] * inv));
     }
     __syncthreads();
     u += n_here;
   }
 }
 
-size_t smem_bytes(int D, int B) {
-  return (CA_WARPS * ROWS * D + CA_WARPS * 2 * ROWS) * sizeof(float) + (B + 1) * sizeof(long long) + (2 * B + 1) * sizeof(int);
+size_t smem_bytes(int D, int rows, int B) {
+  return (CA_WARPS * rows * D + CA_WARPS * 2 * rows) * sizeof(float) + (B + 1) * sizeof(long long) + (2 * B + 1) * sizeof(int);
 }
 
-template <int D, int FMT>
-cudaError_t launch_one(const ChunkAttnParams& p, int grid, cudaStream_t stream) {
-  return launch_pdl(chunk_attn_kernel<D, FMT>, dim3(grid), dim3(CA_THREADS), smem_bytes(D, p.c.B), stream, p);
+template <int D, int FMT, int NT>
+cudaError_t launch_one(const ChunkAttnParams& p, int sms, cudaStream_t stream) {
+  return launch_pdl(chunk_attn_kernel<D, FMT, NT>, dim3(sms * per_sm<D, FMT, NT>()), dim3(CA_THREADS), smem_bytes(D, 8 * NT, p.c.B), stream, p);
 }
 
 template <int D, int FMT>
 cudaError_t setup_one() {
-  return cudaFuncSetAttribute(chunk_attn_kernel<D, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              static_cast<int>(smem_bytes(D, kMaxChunkSlots)));
+  const cudaError_t e = cudaFuncSetAttribute(chunk_attn_kernel<D, FMT, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(smem_bytes(D, 8, kMaxChunkSlots)));
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(chunk_attn_kernel<D, FMT, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              static_cast<int>(smem_bytes(D, 16, kMaxChunkSlots)));
 }
 
 }  // namespace
+
+int chunk_attn_grid_max(int sms) { return 4 * sms; }
+size_t chunk_attn_part_floats(int head_dim, int sms) { return static_cast<size_t>(2) * chunk_attn_grid_max(sms) * part_floats(head_dim); }
 
 cudaError_t setup_chunk_attn(int head_dim, int cache_format) {
   if (head_dim == 64)
@@ -463,14 +511,15 @@ cudaError_t setup_chunk_attn(int head_dim, int cache_format) {
   return cache_format == SDV_CACHE_BF16 ? setup_one<128, SDV_CACHE_BF16>() : setup_one<128, SDV_CACHE_E4M3>();
 }
 
-int chunk_attn_grid(int, int, int sms) { return 2 * sms; }
-
-cudaError_t launch_chunk_attn(int head_dim, int cache_format, const ChunkAttnParams& p, int grid, cudaStream_t stream) {
-  if (head_dim == 64)
-    return cache_format == SDV_CACHE_BF16 ? launch_one<64, SDV_CACHE_BF16>(p, grid, stream)
-                                          : launch_one<64, SDV_CACHE_E4M3>(p, grid, stream);
-  return cache_format == SDV_CACHE_BF16 ? launch_one<128, SDV_CACHE_BF16>(p, grid, stream)
-                                        : launch_one<128, SDV_CACHE_E4M3>(p, grid, stream);
+cudaError_t launch_chunk_attn(int head_dim, int cache_format, bool eight, const ChunkAttnParams& p, int sms, cudaStream_t stream) {
+#define SDV_CHUNK(D, F) return eight ? launch_one<D, F, 1>(p, sms, stream) : launch_one<D, F, 2>(p, sms, stream)
+  if (head_dim == 64) {
+    if (cache_format == SDV_CACHE_BF16) SDV_CHUNK(64, SDV_CACHE_BF16);
+    SDV_CHUNK(64, SDV_CACHE_E4M3);
+  }
+  if (cache_format == SDV_CACHE_BF16) SDV_CHUNK(128, SDV_CACHE_BF16);
+  SDV_CHUNK(128, SDV_CACHE_E4M3);
+#undef SDV_CHUNK
 }
 
 }  // namespace sdv

@@ -656,7 +656,7 @@ __global__ void __launch_bounds__(Cfg<D, FMT>::THREADS, 1)
         set_status(p.c.status, SDV_ERR_TIMEOUT);
         dead = true;
       }
-      dead = __any_sync(0xffffffffu, dead);
+      __syncwarp();
       tc_fence_after();
     };
     walk([&](const SeqRows& s, int, int h, const Item& it, long long u0, int b0, int b1) {
@@ -704,27 +704,35 @@ __global__ void __launch_bounds__(Cfg<D, FMT>::THREADS, 1)
       }
       for (int j = x.s0; j < x.s1; ++j, ++n) {
         wait(&s_full[2 * t + (n & 1)], (n >> 1) & 1);
-        if (dead) break;
         const uint32_t t_sb = t_s + (n & 1) * SK;
         const int key0 = it.page_lo * kPage + j * SK;
-        const bool full_block = key0 + SK - 1 <= x.pmin && (window <= 0 || key0 > x.pmax - window);
-        const int rel = pos - key0;  // key column c is seen when c <= rel and c > rel - window
-        const int low = window > 0 ? rel - window : -0x40000000;
+        // key column c is seen when c <= rel and c > rel - window
+        const bool cut = key0 + SK - 1 > x.pmin || (window > 0 && key0 <= x.pmax - window);
+        const int rel = pos - key0;
         uint32_t buf[2][32];
-        auto mask = [&](uint32_t (&r)[32], int c0) {
-          if (!full_block) {
+        if (cut) {
+          // hide what is not seen, in TMEM, so that what follows is one code for all steps
 #pragma unroll
-            for (int c = 0; c < 32; ++c)
-              if (c0 + c > rel || c0 + c <= low) r[c] = 0xFF800000u;
+          for (int c = 0; c < SK / 32; ++c) {
+            tmem_ld32(t_sb + 32 * c, buf[0]);
+            tmem_wait_ld(buf[0]);
+            // bit e of `see`: column 32 c + e is seen
+            const int hi = rel - 32 * c, lo = window > 0 ? hi - window : -1;
+            uint32_t see = hi < 0 ? 0u : hi >= 31 ? 0xFFFFFFFFu : (2u << hi) - 1u;
+            if (lo >= 0) see &= lo >= 31 ? 0u : 0xFFFFFFFFu << (lo + 1);
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!((see >> e) & 1u)) buf[0][e] = 0xFF800000u;
+            tmem_st32(t_sb + 32 * c, buf[0]);
           }
-        };
-        auto row_top = [&]() {  // the block's largest logit
+          tmem_wait_st();
+        }
+        auto row_top = [&]() {  // the step's largest logit
           float v = -INFINITY;
 #pragma unroll
           for (int c = 0; c < SK / 32; ++c) {
             tmem_ld32(t_sb + 32 * c, buf[0]);
             tmem_wait_ld(buf[0]);
-            mask(buf[0], 32 * c);
 #pragma unroll
             for (int k = 0; k < 32; k += 2) v = fmaxf(v, fmaxf(__uint_as_float(buf[0][k]), __uint_as_float(buf[0][k + 1])));
           }
@@ -741,7 +749,6 @@ __global__ void __launch_bounds__(Cfg<D, FMT>::THREADS, 1)
             tmem_wait_ld(buf[c & 1]);
             if (c + 1 < SK / 32) tmem_ld32(t_sb + 32 * (c + 1), buf[(c + 1) & 1]);
             uint32_t (&r)[32] = buf[c & 1];
-            mask(r, 32 * c);
 #pragma unroll
             for (int k = 0; k < 32; k += 2) {
               float a, b;
@@ -760,10 +767,13 @@ __global__ void __launch_bounds__(Cfg<D, FMT>::THREADS, 1)
           float total, other;
           unf2(add2(sum[0], sum[1]), total, other);
           total += other;
-          if (again || !__any_sync(0xffffffffu, !(total <= kMost))) {
+          // (a wait that has run out is voted on here too, so that the warp stays one)
+          if (!__any_sync(0xffffffffu, (!again && !(total <= kMost)) || dead)) {
             l += total;
             break;
           }
+          dead = __any_sync(0xffffffffu, dead);
+          if (dead) break;
           // a row's weights have grown past what its bound allows (or are not
           // numbers): move the bounds up and take the block again
           const float mn = fmaxf(m, row_top()), f = fast_ex2(m - mn);
@@ -789,6 +799,7 @@ __global__ void __launch_bounds__(Cfg<D, FMT>::THREADS, 1)
             tmem_wait_st();
           }
         }
+        if (dead) break;
         tmem_st32(t_sb, pw);
         tmem_wait_st();
         tc_fence_before();
@@ -798,6 +809,7 @@ __global__ void __launch_bounds__(Cfg<D, FMT>::THREADS, 1)
       if (x.s0 < x.s1) {
         wait(&o_full[t], oph);
         oph ^= 1;
+        dead = __any_sync(0xffffffffu, dead);
       }
       // the blocks that hold a part of this item
       const int c_first = static_cast<int>(u0 / per_cta), c_last = static_cast<int>((u0 + it.blocks - 1) / per_cta);
