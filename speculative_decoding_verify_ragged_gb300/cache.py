@@ -21,11 +21,14 @@ from __future__ import annotations
 
 import ctypes
 
+import torch
+
 from . import SdvError, _ptr, _stream
 from ._abi import (SDV_CACHE_BF16, SDV_CACHE_E4M3, SDV_OK, SdvAppendRows, SdvCacheConfig, SdvChunk, load_library)
 
 __all__ = ["PagedCache", "Chunk"]
 
+BF16, BOTH = (torch.bfloat16,), (torch.bfloat16, torch.float32)
 FORMATS = {"bf16": SDV_CACHE_BF16, "e4m3": SDV_CACHE_E4M3}
 
 
@@ -49,7 +52,6 @@ class PagedCache:
     """
 
     def __init__(self, cfg: dict, max_rows: int, max_slots: int, lib_path: str | None = None):
-        import torch
         self.lib = load_library(lib_path) if lib_path else load_library()
         fmt = cfg.get("cache_format", "bf16")
         if fmt not in FORMATS:
@@ -63,6 +65,9 @@ class PagedCache:
             raise SdvError(1, "sdv_cache_workspace_size rejected the configuration")
         self.workspace = torch.empty(int(nbytes), dtype=torch.uint8, device="cuda")
         self.device = self.workspace.device
+        self._index = self.workspace.get_device()
+        self._append_rows = SdvAppendRows()
+        self._append_ref = ctypes.byref(self._append_rows)
         h = ctypes.c_void_p()
         self._check(self.lib.sdv_cache_create(ctypes.byref(self.cfg), _ptr(self.workspace), ctypes.c_size_t(nbytes),
                                               self.max_rows, self.max_slots, _stream(None), ctypes.byref(h)),
@@ -98,21 +103,26 @@ class PagedCache:
     def _rows(self, t, name, heads, rows, dtypes):
         """The row stride of a [>= rows, heads, head_dim] tensor whose heads are contiguous."""
         d = self.cfg.head_dim
+        n, st = t.shape, t.stride()
+        if len(n) == 3 and t.dtype in dtypes and t.get_device() == self._index and n[0] >= rows and n[1] == heads \
+                and n[2] == d and st[2] == 1 and (st[1] == d or heads == 1):
+            return st[0] if n[0] > 1 else max(st[0], heads * d)
         if t.dtype not in dtypes:
             raise ValueError(f"{name}: {t.dtype}, one of {dtypes} is wanted")
-        if t.device != self.device:
+        if t.get_device() != self._index:
             raise ValueError(f"{name}: on {t.device}, the cache's operators run on {self.device}")
-        s = t.shape
-        if len(s) != 3 or s[0] < rows or s[1] != heads or s[2] != d:
-            raise ValueError(f"{name}: shape {tuple(s)}, [{rows}, {heads}, {d}] is wanted")
-        st = t.stride()
-        if st[2] != 1 or (heads > 1 and st[1] != d):
-            raise ValueError(f"{name}: strides {tuple(st)}: a row's heads must be contiguous")
-        return st[0] if s[0] > 1 else max(st[0], heads * d)
+        if len(n) != 3 or n[0] < rows or n[1] != heads or n[2] != d:
+            raise ValueError(f"{name}: shape {tuple(n)}, [{rows}, {heads}, {d}] is wanted")
+        raise ValueError(f"{name}: strides {tuple(st)}: a row's heads must be contiguous")
+
+    def _enqueue(self, status, stream):
+        """The status word's address and the stream's handle (the current stream's by default)."""
+        if status.dtype is not torch.int32 or status.get_device() != self._index:
+            raise ValueError(f"status: {status.dtype} on {status.device}, int32 on {self.device} is wanted")
+        return status.data_ptr(), torch._C._cuda_getCurrentRawStream(self._index) if stream is None else stream.cuda_stream
 
     def new_pool(self, pages: int):
         """(kv_pool, kv_scales) of a cache of `pages` pages; kv_scales is None for bf16."""
-        import torch
         shape = (int(pages), self.cfg.n_kv, 2, self.cfg.page_size, self.cfg.head_dim)
         if self.format == "bf16":
             return torch.zeros(shape, dtype=torch.bfloat16, device=self.device), None
@@ -122,7 +132,6 @@ class PagedCache:
     def chunk(self, rows: int, max_q: int, row_offsets, kv_lens, page_table, kv_pool, kv_scales=None,
               window: int = 0) -> Chunk:
         """Describe a ragged chunk (sdv_chunk): `rows` rows of at most `max_q` per sequence."""
-        import torch
         B = int(kv_lens.shape[0])
         self._want(kv_lens, "kv_lens", torch.int32, (B,))
         self._want(row_offsets, "row_offsets", torch.int32, (B + 1,))
@@ -146,40 +155,46 @@ class PagedCache:
     def append(self, chunk: Chunk, k, v, status, q=None, q_out=None, stream=None):
         """Store the chunk's k, v [T, n_kv, head_dim] (bf16 or fp32, rows strided), rotated where the cache
         rotates; with q [T, n_q, head_dim] also its rotation in bf16 into q_out."""
-        import torch
-        self._want(status, "status", torch.int32)
-        c, T, io = self.cfg, chunk.rows, (k.dtype,)
-        ks = self._rows(k, "k", c.n_kv, T, (torch.bfloat16, torch.float32))
-        vs = self._rows(v, "v", c.n_kv, T, io)
-        if (q is None) != (q_out is None):
+        c, T, r = self.cfg, chunk.rows, self._append_rows
+        io = (k.dtype,)
+        r.k_stride = self._rows(k, "k", c.n_kv, T, BOTH)
+        r.v_stride = self._rows(v, "v", c.n_kv, T, io)
+        r.k, r.v, r.x_format = k.data_ptr(), v.data_ptr(), 1 if k.dtype is torch.float32 else 0
+        if q is None and q_out is None:
+            r.q = r.q_out = None
+        elif q is None or q_out is None:
             raise ValueError("q and q_out come together")
-        qs = self._rows(q, "q", c.n_q, T, io) if q is not None else 0
-        qos = self._rows(q_out, "q_out", c.n_q, T, (torch.bfloat16,)) if q is not None else 0
-        rows = SdvAppendRows(k.data_ptr(), v.data_ptr(), q.data_ptr() if q is not None else None, ks, vs, qs,
-                             1 if k.dtype == torch.float32 else 0, q_out.data_ptr() if q is not None else None, qos)
-        self._check(self.lib.sdv_cache_append(self.handle, chunk.ref, ctypes.byref(rows), _ptr(status), _stream(stream)),
-                    "sdv_cache_append")
+        else:
+            r.q_stride = self._rows(q, "q", c.n_q, T, io)
+            r.q_out_stride = self._rows(q_out, "q_out", c.n_q, T, BF16)
+            r.q, r.q_out = q.data_ptr(), q_out.data_ptr()
+        st, raw = self._enqueue(status, stream)
+        rc = self.lib.sdv_cache_append(self.handle, chunk.ref, self._append_ref, st, raw)
+        if rc:
+            self._check(rc, "sdv_cache_append")
 
     def attention(self, chunk: Chunk, q, out, status, stream=None):
         """Attention of q [T, n_q, head_dim] bf16 over the cached positions each row sees, into out."""
-        import torch
-        self._want(status, "status", torch.int32)
-        c, T, io = self.cfg, chunk.rows, (torch.bfloat16,)
-        qs, os_ = self._rows(q, "q", c.n_q, T, io), self._rows(out, "out", c.n_q, T, io)
-        self._check(self.lib.sdv_cache_attention(self.handle, chunk.ref, _ptr(q), qs, _ptr(out), os_, _ptr(status),
-                                                 _stream(stream)), "sdv_cache_attention")
+        n_q, T = self.cfg.n_q, chunk.rows
+        qs, os_ = self._rows(q, "q", n_q, T, BF16), self._rows(out, "out", n_q, T, BF16)
+        st, raw = self._enqueue(status, stream)
+        rc = self.lib.sdv_cache_attention(self.handle, chunk.ref, q.data_ptr(), qs, out.data_ptr(), os_, st, raw)
+        if rc:
+            self._check(rc, "sdv_cache_attention")
 
     def read(self, chunk: Chunk, k_out, v_out, status, stream=None):
         """Read the chunk's positions back into k_out, v_out [T, n_kv, head_dim] (bf16 or fp32; either may be None)."""
-        import torch
-        self._want(status, "status", torch.int32)
-        c, T = self.cfg, chunk.rows
+        n_kv, T = self.cfg.n_kv, chunk.rows
         first = k_out if k_out is not None else v_out
         if first is None:
             raise ValueError("k_out, v_out: one of them is wanted")
-        io = (first.dtype,) if first.dtype in (torch.bfloat16, torch.float32) else (torch.bfloat16, torch.float32)
-        ks = self._rows(k_out, "k_out", c.n_kv, T, io) if k_out is not None else 0
-        vs = self._rows(v_out, "v_out", c.n_kv, T, io) if v_out is not None else 0
-        self._check(self.lib.sdv_cache_read(self.handle, chunk.ref, _ptr(k_out), ks, _ptr(v_out), vs,
-                                            1 if first.dtype == torch.float32 else 0, _ptr(status), _stream(stream)),
-                    "sdv_cache_read")
+        kp = vp = None
+        ks = vs = 0
+        if k_out is not None:
+            ks, kp = self._rows(k_out, "k_out", n_kv, T, BOTH), k_out.data_ptr()
+        if v_out is not None:
+            vs, vp = self._rows(v_out, "v_out", n_kv, T, BOTH if k_out is None else (k_out.dtype,)), v_out.data_ptr()
+        st, raw = self._enqueue(status, stream)
+        rc = self.lib.sdv_cache_read(self.handle, chunk.ref, kp, ks, vp, vs, 1 if first.dtype is torch.float32 else 0, st, raw)
+        if rc:
+            self._check(rc, "sdv_cache_read")

@@ -11,6 +11,7 @@ struct sdv_cache {
   int device, sms, max_rows, max_slots;
   float *part, *part_tc;
   int *counters, *counters_tc;
+  int4* cuts;
   sdv::RopeTurns turns;
 };
 
@@ -37,13 +38,14 @@ int sms_of(int dev) {
 constexpr int kSmallRows = 16;
 
 struct Space {
-  size_t counters, counters_tc, part, part_tc, total;
+  size_t counters, counters_tc, cuts, part, part_tc, total;
 };
 Space space(const sdv_cache_config& c, int sms) {
   Space s{};
   s.counters = 0;
   s.counters_tc = up256(chunk_attn_grid_max(sms) * sizeof(int));
-  s.part = s.counters_tc + up256(2 * sms * sizeof(int));
+  s.cuts = s.counters_tc + up256(2 * sms * sizeof(int));
+  s.part = s.cuts + up256(2 * sms * sizeof(int4));
   s.part_tc = s.part + up256(chunk_attn_part_floats(c.head_dim, sms) * sizeof(float));
   s.total = s.part_tc + up256(chunk_attn_tc_part_floats(c.head_dim, sms) * sizeof(float));
   return s;
@@ -125,6 +127,7 @@ extern "C" sdv_status sdv_cache_create(const sdv_cache_config* cfg, void* worksp
   h->max_slots = max_slots;
   h->counters = reinterpret_cast<int*>(static_cast<uint8_t*>(workspace) + s.counters);
   h->counters_tc = reinterpret_cast<int*>(static_cast<uint8_t*>(workspace) + s.counters_tc);
+  h->cuts = reinterpret_cast<int4*>(static_cast<uint8_t*>(workspace) + s.cuts);
   h->part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + s.part);
   h->part_tc = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + s.part_tc);
   for (int j = 0; j < 64; ++j) {
@@ -193,8 +196,13 @@ extern "C" sdv_status sdv_cache_attention(sdv_cache* h, const sdv_chunk* chunk, 
   const int group = h->cfg.n_q / h->cfg.n_kv;
   const long long rows = (long long)(chunk->max_q < chunk->T ? chunk->max_q : chunk->T) * group;  // of a sequence at most
   if (rows > kSmallRows) {
-    p.small_rows = kSmallRows;
+    // The tcgen05 kernel takes every sequence, but where most must be far
+    // shorter than the longest (a step that mixes next tokens with pieces of
+    // prompts): there the mma.sync kernel takes those of few rows
+    const bool two = chunk->B >= 8 && chunk->T <= (long long)chunk->B * chunk->max_q / 2;
+    p.small_rows = two ? kSmallRows : 0;
     p.part = h->part_tc;
+    p.cuts = h->cuts;
     p.counters = h->counters_tc;
     CUtensorMap map;
     if (h->cfg.cache_format == SDV_CACHE_BF16) {
@@ -204,6 +212,7 @@ extern "C" sdv_status sdv_cache_attention(sdv_cache* h, const sdv_chunk* chunk, 
     }
     const cudaError_t e = launch_chunk_attn_tc(d, h->cfg.cache_format, map, p, h->sms, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e);
+    if (!two) return SDV_OK;
   }
   p.part = h->part;
   p.counters = h->counters;

@@ -122,6 +122,7 @@ struct ChunkAttnParams {
   long long q_stride = 0, out_stride = 0;
   float* part = nullptr;     // partial results of cut items, two per block of the launch
   int* counters = nullptr;   // arrivals at them, zero between launches
+  int4* cuts = nullptr;      // tcgen05: [2 * blocks] the item of many parts that begins in each run
   int small_rows = 0;        // packed rows up to which a sequence is the mma.sync kernel's
   float scale_log2 = 0.f;    // log2(e) / sqrt(head_dim)
 };

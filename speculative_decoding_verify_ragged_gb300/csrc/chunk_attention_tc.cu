@@ -3,8 +3,8 @@
 //
 // An item is two tiles of 128 packed query rows (row = token, head of the group)
 // of one (sequence, key head) against the blocks of 128 keys that they see.  The
-// items' blocks are laid end to end and cut into equal runs, one per SM; an item
-// cut between SMs is joined, in SM order, by the last to arrive.  Per block
+// items' blocks are laid end to end and cut into equal runs, one per SM; the
+// parts of an item cut between SMs are joined in the runs' order.  Per block
 //   S_t = Q_t K^T  (M = 128 rows, N = 128 keys),  O_t += P_t V  (P_t from TMEM)
 // run for tile 0 and tile 1 in turn, so the tensor cores work on one tile while
 // the other's softmax runs: one thread holds one row, reads its scores from
@@ -36,6 +36,7 @@ constexpr float kNoMax = -1e30f;     // the bound before the first visible key, 
 // A row's weights of one step may add up to this before its bound moves: each
 // then fits fp16, and no maximum is taken in the steps between.
 constexpr float kMost = 16384.f;
+constexpr int kJoinHere = 4;         // an item of up to this many parts more than one is joined by its last block
 
 constexpr int MMA_WARP = 8, TMA_WARP = 10, CONV_WARP = 12;  // MMA_WARP + t issues tile t's products, TMA_WARP + 1 copies V
 
@@ -217,10 +218,30 @@ __device__ __forceinline__ Tile make_tile(const SeqRows& s, const Item& it, int 
   return x;
 }
 
-// A place in the walk over all items' blocks: sequence, key head, item, block.
+// What a block of the item costs: its tiles; and an item before its first block
+// (query, first scores, output: about two blocks' time, which without it left
+// the SMs with the short items at the end: 4096 new tokens 193 -> 136 us).
+__device__ __forceinline__ int weight(const Item& it) { return it.rows > BM ? 2 : 1; }
+constexpr int kItemCost = 6;
+__device__ __forceinline__ int units_of(const Item& it) { return kItemCost + it.blocks * weight(it); }
+
+// A part of a run: blocks [b0, b1) of an item of (sequence b, key head h) whose first unit is u0.
+struct Part {
+  SeqRows s;
+  Item it;
+  int b, h, qt, b0, b1;
+  long long u0;
+};
 struct Place {
   int b, h, qt, blk;
+  long long u0;
 };
+
+// Where run `cta` leaves its part of tile t of the item that begins in run
+// c_first: a run has two at most, of an item begun before it and of one that goes on behind it.
+__device__ __forceinline__ float* part_slot(float* part, int D, int cta, int c_first, int t) {
+  return part + ((2LL * cta + (cta == c_first)) * 2 + t) * ((long long)BM * (D + 2));
+}
 
 template <int D, int FMT>
 __global__ void __launch_bounds__(Cfg<D, FMT>::THREADS, 1)
@@ -239,8 +260,10 @@ __global__ void __launch_bounds__(Cfg<D, FMT>::THREADS, 1)
   uint64_t* tail = o_full + 2;       // copies of a block whose end is zeroed before use
   uint64_t* done = tail + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
-  __shared__ long long s_scan[2];        // first unit of the sequence the run starts in; units of the launch
+  __shared__ long long s_scan[2];  // units of a run; of the launch
   __shared__ Place s_start;
+  __shared__ Part s_part[8];       // the softmax warps' place in the run, out of their registers
+  __shared__ int s_flag[2][2];     // [tile][turn] whether the others' parts of an item are all there
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
@@ -281,28 +304,31 @@ __global__ void __launch_bounds__(Cfg<D, FMT>::THREADS, 1)
   auto items_of = [&](const SeqRows& s) { return (int)(((long long)s.n * group + 2 * BM - 1) / (2 * BM)); };
 
   // ---- the chunk's check and this block's run of units ----
-  const int status0 = read_status(p.c.status);
-  const bool dead0 = __syncthreads_or(status0 != 0);  // one verdict for the block
-  bool good;
+  bool good, dead0;
   {
     int bad = 0;
+    const int status0 = read_status(p.c.status);
     for (int b = tid; b < B; b += blockDim.x) {
       const int o = p.c.row_offsets[b], e = p.c.row_offsets[b + 1], len = p.c.kv_lens[b];
       if (o < 0 || e < o || e > p.c.T || e - o > p.c.max_q || (b == 0 && o != 0) || len < 0) bad |= 1;
       if (len > (long long)p.c.max_pages * kPage) bad |= 2;
     }
     const bool b1 = __syncthreads_or(bad & 1), b2 = __syncthreads_or(bad & 2);
+    dead0 = __syncthreads_or(status0 != 0);  // one verdict for the block
     if ((b1 || b2) && tid == 0) set_status(p.c.status, b1 ? SDV_ERR_BAD_INPUT : SDV_ERR_PAGE_RANGE);
     good = !b1 && !b2;
+    if (tid == 0) p.cuts[2 * blockIdx.x].x = -1;  // no item begins here and goes on, so far
   }
   long long u_begin = 0, u_end = 0, per_cta = 1;
   if (good) {
-    // blocks of one key head of each sequence, a warp a sequence, into the ring (not in use yet)
+    // units (blocks times tiles) of one key head of each sequence, a warp a sequence, into the ring (not in use yet)
     int* s_units = reinterpret_cast<int*>(smem);                                                 // [B]
     for (int b = warp; b < B; b += blockDim.x / kWarp) {
       const SeqRows s = seq_of(b);
       int sum = 0;
-      for (int qt = lane; qt < items_of(s); qt += kWarp) sum += make_item(s, group, window, qt).blocks;
+      for (int qt = lane; qt < items_of(s); qt += kWarp) {
+        sum += units_of(make_item(s, group, window, qt));
+      }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
       if (lane == 0) s_units[b] = sum;
@@ -317,7 +343,8 @@ __global__ void __launch_bounds__(Cfg<D, FMT>::THREADS, 1)
         for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
         total += v;
       }
-      const long long per = max(1LL, (total + gridDim.x - 1) / gridDim.x), u = (long long)blockIdx.x * per;
+      const long long per = max(2LL, (total + gridDim.x - 1) / gridDim.x);  // two: a block of two tiles begins in every run
+      const long long u = (long long)blockIdx.x * per;
       if (u < total) {
         long long base = 0;
         int b = -1;
@@ -342,7 +369,7 @@ __global__ void __launch_bounds__(Cfg<D, FMT>::THREADS, 1)
         const int per_head = s_units[b], h = static_cast<int>((u - base) / per_head);
         int rest = static_cast<int>((u - base) - (long long)h * per_head), qt = -1;
         for (int q0 = 0; qt < 0; q0 += kWarp) {
-          const int v = q0 + lane < items_of(s) ? make_item(s, group, window, q0 + lane).blocks : 0;
+          const int v = q0 + lane < items_of(s) ? units_of(make_item(s, group, window, q0 + lane)) : 0;
           int inc = v;
 #pragma unroll
           for (int o = 1; o < 32; o <<= 1) {
@@ -358,7 +385,11 @@ __global__ void __launch_bounds__(Cfg<D, FMT>::THREADS, 1)
             rest -= __shfl_sync(0xffffffffu, inc, 31);
           }
         }
-        if (lane == 0) s_start = Place{b, h, qt, rest};
+        if (lane == 0) {
+          // the first block that begins at the run's first unit or behind it
+          const int w = weight(make_item(s, group, window, qt));
+          s_start = Place{b, h, qt, (max(0, rest - kItemCost) + w - 1) / w, u - rest};
+        }
       }
       if (lane == 0) {
         s_scan[0] = per;
@@ -371,27 +402,43 @@ __global__ void __launch_bounds__(Cfg<D, FMT>::THREADS, 1)
     u_begin = (long long)blockIdx.x * per_cta;
     u_end = min(s_scan[1], u_begin + per_cta);
   }
-  // calls f(sequence, key head, item, its first unit, blocks [b0, b1) of this run) for each part of the run
-  auto walk = [&](auto&& f) {
-    if (u_begin >= u_end) return;
-    Place at = s_start;
-    SeqRows s = seq_of(at.b);
-    for (long long u = u_begin;;) {
-      const Item it = make_item(s, group, window, at.qt);
-      const int n = static_cast<int>(min((long long)(it.blocks - at.blk), u_end - u));
-      if (!f(s, at.b, at.h, it, u - at.blk, at.blk, at.blk + n)) return;
-      u += n;
-      if (u >= u_end) return;
-      at.blk = 0;
-      if (++at.qt == items_of(s)) {
-        at.qt = 0;
-        if (++at.h == n_kv) {
-          at.h = 0;
-          do s = seq_of(++at.b);
-          while (s.n == 0);
+  // the parts of the run, one after another; a block is of the run that its first unit falls in
+  auto end_block = [&](const Part& x) {  // blocks of x that begin before the run's end
+    const int w = weight(x.it);
+    return static_cast<int>(min((long long)x.it.blocks, max(0LL, u_end - x.u0 - kItemCost + w - 1) / w));
+  };
+  auto next_part = [&](Part& x) {
+    {
+      x.u0 += units_of(x.it);
+      if (x.u0 >= u_end) return false;
+      x.b0 = 0;
+      if (++x.qt == items_of(x.s)) {
+        x.qt = 0;
+        if (++x.h == n_kv) {
+          x.h = 0;
+          do x.s = seq_of(++x.b);
+          while (x.s.n == 0);
         }
       }
+      x.it = make_item(x.s, group, window, x.qt);
+      x.b1 = end_block(x);
+      if (x.b1 == 0) return false;
+      return true;
     }
+  };
+  auto first_part = [&](Part& x) {
+    if (u_begin >= u_end) return false;
+    const Place at = s_start;
+    x.b = at.b, x.h = at.h, x.qt = at.qt, x.b0 = at.blk, x.u0 = at.u0;
+    x.s = seq_of(x.b);
+    x.it = make_item(x.s, group, window, x.qt);
+    x.b1 = end_block(x);
+    return x.b0 < x.b1 || next_part(x);
+  };
+  auto walk = [&](auto&& f) {
+    Part x;
+    for (bool more = first_part(x); more; more = next_part(x))
+      if (!f(x.s, x.b, x.h, x.it, x.b0, x.b1)) return;
   };
   auto clip = [](Tile x, int b0, int b1) {  // the tile's steps within blocks [b0, b1)
     x.s0 = max(x.s0, 2 * b0);
@@ -428,7 +475,7 @@ __global__ void __launch_bounds__(Cfg<D, FMT>::THREADS, 1)
         phase ^= 1;
       }
     };
-    walk([&](const SeqRows& s, int b, int h, const Item& it, long long, int b0, int b1) {
+    walk([&](const SeqRows& s, int b, int h, const Item& it, int b0, int b1) {
       const Tile t0 = clip(make_tile(s, it, group, window, 0), b0, b1), t1 = clip(make_tile(s, it, group, window, 1), b0, b1);
       const int2 used = both(t0, t1);
       if (used.x >= used.y || dead) return !dead;
@@ -579,7 +626,7 @@ __global__ void __launch_bounds__(Cfg<D, FMT>::THREADS, 1)
           ph ^= 1;
         }
       };
-      walk([&](const SeqRows& s, int, int, const Item& it, long long, int b0, int b1) {
+      walk([&](const SeqRows& s, int, int, const Item& it, int b0, int b1) {
         const Tile t0 = clip(make_tile(s, it, group, window, 0), b0, b1), t1 = clip(make_tile(s, it, group, window, 1), b0, b1);
         const int2 used = both(t0, t1);
         const int first = t ? t1.s0 : t0.s0, last = t ? t1.s1 : t0.s1;
@@ -659,21 +706,49 @@ __global__ void __launch_bounds__(Cfg<D, FMT>::THREADS, 1)
       __syncwarp();
       tc_fence_after();
     };
-    walk([&](const SeqRows& s, int, int h, const Item& it, long long u0, int b0, int b1) {
-      const Tile whole = make_tile(s, it, group, window, t), x = clip(whole, b0, b1);
-      const int row = it.row0 + t * BM + i;
-      const bool in = i < whole.rows;
-      const int pos = in ? s.pos0 + row / group : -1;
-      const long long tok = s.off + (in ? row / group : 0);
-      const int head = h * group + (in ? row % group : 0);
-      float cz = p.scale_log2, m = kNoMax, l = 0.f;
+    // An item's output is taken from TMEM only after the next item's query is on
+    // its way, so that the next scores are made meanwhile.
+    bool held = false, in = false, went = false;  // an item whose output is still in TMEM: its row exists; it had steps
+    int turn = 0;
+    int c_first = 0, c_last = 0;                  // the blocks that hold a part of it
+    __nv_bfloat16* dst = nullptr;
+    float m = kNoMax, l = 0.f;
+    for (bool more = true;;) {
+      Part part;
+      if (held) {
+        part = s_part[warp];
+        more = next_part(part);
+      } else {
+        more = first_part(part);
+      }
+      __syncwarp();
+      if (lane == 0) s_part[warp] = part;
+      __syncwarp();
+      if (!more && !held) break;
+      const SeqRows& s = part.s;
+      const Item& it = part.it;
+      Tile x;
+      x.s0 = x.s1 = 0;
+      bool in_next = false;
+      int row = 0;
+      float cz = p.scale_log2;
+      long long tok = 0;
+      int head = 0;
+      if (more) {
+        const Tile whole = make_tile(s, it, group, window, t);
+        x = clip(whole, part.b0, part.b1);
+        row = it.row0 + t * BM + i;
+        in_next = i < whole.rows;
+        tok = s.off + (in_next ? row / group : 0);
+        head = part.h * group + (in_next ? row % group : 0);
+      }
       if (x.s0 < x.s1 && !dead) {
-        // this row's query into the tile (its last reader, the item before, is done: its scores were all read)
+        // this row's query into the tile (its last readers are done: the scores were all seen)
         const uint4* src = reinterpret_cast<const uint4*>(p.q + tok * p.q_stride + (long long)head * D);
-        uint8_t* dst = smem + C::OFF_Q + t * C::SLOT + i * 128;
+        uint8_t* q_row = smem + C::OFF_Q + t * C::SLOT + i * 128;
         uint4 w[D / 8];
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) w[c] = in ? src[c] : make_uint4(0u, 0u, 0u, 0u);
+        for (int c = 0; c < D / 8; ++c) w[c] = in_next ? src[c] : make_uint4(0u, 0u, 0u, 0u);
         if constexpr (C::kCodes) {
           // fp16 with the row's largest magnitude in [1/2, 1)
           float a = 0.f;
@@ -697,11 +772,146 @@ __global__ void __launch_bounds__(Cfg<D, FMT>::THREADS, 1)
           }
         }
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) *reinterpret_cast<uint4*>(dst + (c >> 3) * HALF + (((c & 7) ^ (i & 7)) << 4)) = w[c];
+        for (int c = 0; c < D / 8; ++c) *reinterpret_cast<uint4*>(q_row + (c >> 3) * HALF + (((c & 7) ^ (i & 7)) << 4)) = w[c];
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&q_full[t]);
       }
+      if (held) {
+        if (went) {
+          wait(&o_full[t], oph);
+          oph ^= 1;
+          dead = __any_sync(0xffffffffu, dead);
+        }
+        const int others = c_last - c_first;
+        bool join = false, write = in && !dead;
+        if (others > 0) {
+          // A part: [column][row], then bounds and sums.  Items of few parts are
+          // joined here by the last to arrive, whose own part need not leave TMEM
+          // (of an item's two parts the one begun earlier ends later as a rule);
+          // those of many by chunk_join_kernel, which spreads them over the GPU.
+          join = others <= kJoinHere;
+          int* count = p.counters + 2 * c_first + t;
+          bool last = false;
+          if (join) {
+            turn ^= 1;
+            if (i == 0) {
+              s_flag[t][turn] = atomicAdd(count, 0) == others;
+              __threadfence();
+            }
+            named_sync(1 + t, BM);
+            last = *reinterpret_cast<volatile int*>(&s_flag[t][turn]) != 0;
+          }
+          if (!last) {
+            float* mine = part_slot(p.part, D, blockIdx.x, c_first, t);
+            if (went && !dead) {
+#pragma unroll
+              for (int c = 0; c < D / 32; ++c) {
+                uint32_t r[32];
+                tmem_ld32(t_o + 32 * c, r);
+                tmem_wait_ld(r);
+#pragma unroll
+                for (int k = 0; k < 32; ++k) mine[(32 * c + k) * BM + i] = __uint_as_float(r[k]);
+              }
+            }
+            mine[D * BM + i] = m;
+            mine[(D + 1) * BM + i] = l;
+            if (join) {
+              turn ^= 1;
+              __threadfence();
+              named_sync(1 + t, BM);
+              if (i == 0) {
+                s_flag[t][turn] = atomicAdd(count, 1) == others;
+                __threadfence();
+              }
+              named_sync(1 + t, BM);
+              last = *reinterpret_cast<volatile int*>(&s_flag[t][turn]) != 0;
+            }
+          }
+          if (last && i == 0) *count = 0;
+          write = write && last;
+        }
+        // this part's share of the row, and the others'
+        float f[kJoinHere + 1];
+        if (join && write) {
+          float mk[kJoinHere + 1], lk[kJoinHere + 1], top = kNoMax;
+#pragma unroll
+          for (int k = 0; k <= kJoinHere; ++k) {
+            mk[k] = kNoMax;
+            lk[k] = 0.f;
+            if (k <= others) {
+              const float* src = part_slot(p.part, D, c_first + k, c_first, t);
+              const bool me = c_first + k == (int)blockIdx.x;
+              mk[k] = me ? m : __ldcg(src + D * BM + i);
+              lk[k] = me ? l : __ldcg(src + (D + 1) * BM + i);
+            }
+          }
+#pragma unroll
+          for (int k = 0; k <= kJoinHere; ++k) top = fmaxf(top, mk[k]);
+          l = 0.f;
+#pragma unroll
+          for (int k = 0; k <= kJoinHere; ++k) {
+            f[k] = lk[k] == 0.f ? 0.f : fast_ex2(mk[k] - top);
+            l += f[k] * lk[k];
+          }
+        }
+        const float inv = l == 0.f ? 0.f : 1.f / l;  // a row that sees nothing gives 0
+        if (others == 0 || __any_sync(0xffffffffu, join && write)) {
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t r[32];
+            if (went && !dead) {
+              tmem_ld32(t_o + 32 * c, r);
+              tmem_wait_ld(r);
+            } else {
+#pragma unroll
+              for (int k = 0; k < 32; ++k) r[k] = 0;
+            }
+            if (join && write) {
+              float acc[32];
+#pragma unroll
+              for (int x = 0; x < 32; ++x) acc[x] = 0.f;
+#pragma unroll
+              for (int k = 0; k <= kJoinHere; ++k)
+                if (k <= others && f[k] != 0.f) {  // (a part that saw nothing wrote no columns)
+                  if (c_first + k == (int)blockIdx.x) {
+#pragma unroll
+                    for (int x = 0; x < 32; ++x) acc[x] += f[k] * __uint_as_float(r[x]);
+                  } else {
+                    const float* src = part_slot(p.part, D, c_first + k, c_first, t) + 32 * c * BM + i;
+#pragma unroll
+                    for (int x = 0; x < 32; ++x) acc[x] += f[k] * __ldcg(src + x * BM);
+                  }
+                }
+#pragma unroll
+              for (int x = 0; x < 32; ++x) r[x] = __float_as_uint(acc[x]);
+            }
+            if (write)
+#pragma unroll
+              for (int k = 0; k < 32; k += 8) {
+                uint32_t o[4];
+#pragma unroll
+                for (int y = 0; y < 4; ++y)
+                  o[y] = l == 0.f ? 0u : pack_bf16x2(__uint_as_float(r[k + 2 * y]) * inv, __uint_as_float(r[k + 2 * y + 1]) * inv);
+                *reinterpret_cast<uint4*>(dst + 32 * c + k) = make_uint4(o[0], o[1], o[2], o[3]);
+              }
+          }
+        }
+        tc_fence_before();
+      }
+      if (!more) break;
+      in = in_next;
+      went = x.s0 < x.s1;
+      dst = p.out + tok * p.out_stride + (long long)head * D;
+      c_first = static_cast<int>((part.u0 + kItemCost) / per_cta);
+      c_last = static_cast<int>((part.u0 + kItemCost + (long long)(it.blocks - 1) * weight(it)) / per_cta);
+      if (tid == 0 && c_last - c_first > kJoinHere && c_first == (int)blockIdx.x) {
+        p.cuts[2 * blockIdx.x] = make_int4(c_last, s.off, part.h, it.row0);
+        p.cuts[2 * blockIdx.x + 1].x = it.rows;
+      }
+      m = kNoMax;
+      l = 0.f;
+      const int pos = in ? s.pos0 + row / group : -1;
       for (int j = x.s0; j < x.s1; ++j, ++n) {
         wait(&s_full[2 * t + (n & 1)], (n >> 1) & 1);
         const uint32_t t_sb = t_s + (n & 1) * SK;
@@ -806,94 +1016,8 @@ __global__ void __launch_bounds__(Cfg<D, FMT>::THREADS, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[2 * t + (n & 1)]);
       }
-      if (x.s0 < x.s1) {
-        wait(&o_full[t], oph);
-        oph ^= 1;
-        dead = __any_sync(0xffffffffu, dead);
-      }
-      // the blocks that hold a part of this item
-      const int c_first = static_cast<int>(u0 / per_cta), c_last = static_cast<int>((u0 + it.blocks - 1) / per_cta);
-      __nv_bfloat16* dst = p.out + tok * p.out_stride + (long long)head * D;
-      if (c_first == c_last) {
-        const float inv = l == 0.f ? 0.f : 1.f / l;  // a row that sees nothing gives 0
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t r[32];
-          if (x.s0 < x.s1 && !dead) {
-            tmem_ld32(t_o + 32 * c, r);
-            tmem_wait_ld(r);
-          } else {
-#pragma unroll
-            for (int k = 0; k < 32; ++k) r[k] = 0;
-          }
-          if (in && !dead)
-#pragma unroll
-            for (int k = 0; k < 32; k += 8) {
-              uint32_t o[4];
-#pragma unroll
-              for (int y = 0; y < 4; ++y)
-                o[y] = l == 0.f ? 0u : pack_bf16x2(__uint_as_float(r[k + 2 * y]) * inv, __uint_as_float(r[k + 2 * y + 1]) * inv);
-              *reinterpret_cast<uint4*>(dst + 32 * c + k) = make_uint4(o[0], o[1], o[2], o[3]);
-            }
-        }
-        tc_fence_before();
-        return true;
-      }
-      // a part: [column][row], then bounds and sums; slot 0 for an item begun before this run, 1 for one that goes on
-      constexpr long long PF = (long long)BM * (D + 2);
-      auto part_of = [&](int cta) { return p.part + ((2LL * cta + (cta == c_first)) * 2 + t) * PF; };
-      float* mine = part_of(blockIdx.x);
-      if (x.s0 < x.s1 && !dead) {
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t r[32];
-          tmem_ld32(t_o + 32 * c, r);
-          tmem_wait_ld(r);
-#pragma unroll
-          for (int k = 0; k < 32; ++k) mine[(32 * c + k) * BM + i] = __uint_as_float(r[k]);
-        }
-        tc_fence_before();
-      }
-      mine[D * BM + i] = m;
-      mine[(D + 1) * BM + i] = l;
-      __threadfence();
-      named_sync(1 + t, BM);
-      int* s_last = reinterpret_cast<int*>(tmem_slot + 1 + t);
-      if (i == 0) {
-        int* count = p.counters + 2 * c_first + t;
-        *s_last = atomicAdd(count, 1) == c_last - c_first;
-        if (*s_last) *count = 0;
-        __threadfence();
-      }
-      named_sync(1 + t, BM);
-      const bool last = *reinterpret_cast<volatile int*>(s_last) != 0;
-      named_sync(1 + t, BM);  // read by all before the next item writes it
-      if (!last || dead || !in) return true;
-      m = kNoMax;
-      for (int cta = c_first; cta <= c_last; ++cta) m = fmaxf(m, __ldcg(part_of(cta) + D * BM + i));
-      l = 0.f;
-      for (int cta = c_first; cta <= c_last; ++cta)
-        l += fast_ex2(__ldcg(part_of(cta) + D * BM + i) - m) * __ldcg(part_of(cta) + (D + 1) * BM + i);
-      const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
-        float acc[32];
-#pragma unroll
-        for (int k = 0; k < 32; ++k) acc[k] = 0.f;
-        for (int cta = c_first; cta <= c_last; ++cta) {
-          const float* src = part_of(cta);
-          if (__ldcg(src + (D + 1) * BM + i) == 0.f) continue;  // it saw nothing and wrote no columns
-          const float f = fast_ex2(__ldcg(src + D * BM + i) - m) * inv;
-#pragma unroll
-          for (int k = 0; k < 32; ++k) acc[k] += f * __ldcg(src + (32 * c + k) * BM + i);
-        }
-#pragma unroll
-        for (int k = 0; k < 32; k += 8)
-          *reinterpret_cast<uint4*>(dst + 32 * c + k) = make_uint4(pack_bf16x2(acc[k], acc[k + 1]), pack_bf16x2(acc[k + 2], acc[k + 3]),
-                                                                   pack_bf16x2(acc[k + 4], acc[k + 5]), pack_bf16x2(acc[k + 6], acc[k + 7]));
-      }
-      return true;
-    });
+      held = true;
+    }
   };
   // a warpgroup changes its registers as one
   if (warp >= CONV_WARP) {
@@ -916,9 +1040,52 @@ __global__ void __launch_bounds__(Cfg<D, FMT>::THREADS, 1)
   }
 }
 
+// Joins the items of many parts (few rows over many keys: up to a part of 128 KB
+// on every SM): block (c, y) takes 16 columns of one tile of the item that
+// begins in run c, a thread a row, parts in order, four parts' loads in flight.
+template <int D>
+__global__ void __launch_bounds__(BM) chunk_join_kernel(const ChunkAttnParams p) {
+  constexpr int COLS = 16;
+  griddep_launch_dependents();
+  griddep_wait();
+  const int c = blockIdx.x, t = blockIdx.y & 1, col = (blockIdx.y >> 1) * COLS, i = threadIdx.x;
+  const int4 cut = p.cuts[2 * c];
+  if (cut.x < 0 || read_status(p.c.status) != 0) return;
+  const int rows = p.cuts[2 * c + 1].x - t * BM, last = cut.x;
+  if (i >= rows) return;
+  const int group = p.c.n_q / p.c.n_kv, row = cut.w + t * BM + i;
+  float m = kNoMax;
+#pragma unroll 8
+  for (int k = c; k <= last; ++k) m = fmaxf(m, part_slot(p.part, D, k, c, t)[D * BM + i]);
+  float l = 0.f, acc[COLS];
+#pragma unroll
+  for (int x = 0; x < COLS; ++x) acc[x] = 0.f;
+#pragma unroll 4
+  for (int k = c; k <= last; ++k) {
+    const float* src = part_slot(p.part, D, k, c, t);
+    const float lk = src[(D + 1) * BM + i], f = fast_ex2(src[D * BM + i] - m);
+    const bool any = lk != 0.f;  // else it saw nothing and wrote no columns
+    l += any ? f * lk : 0.f;
+#pragma unroll
+    for (int x = 0; x < COLS; ++x) {
+      const float v = src[(col + x) * BM + i];
+      acc[x] += any ? f * v : 0.f;
+    }
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  __nv_bfloat16* dst = p.out + (long long)(cut.y + row / group) * p.out_stride + (long long)(cut.z * group + row % group) * D + col;
+#pragma unroll
+  for (int x = 0; x < COLS; x += 8)
+    *reinterpret_cast<uint4*>(dst + x) =
+        make_uint4(pack_bf16x2(acc[x] * inv, acc[x + 1] * inv), pack_bf16x2(acc[x + 2] * inv, acc[x + 3] * inv),
+                   pack_bf16x2(acc[x + 4] * inv, acc[x + 5] * inv), pack_bf16x2(acc[x + 6] * inv, acc[x + 7] * inv));
+}
+
 template <int D, int FMT>
 cudaError_t launch_one(const CUtensorMap& map, const ChunkAttnParams& p, int grid, cudaStream_t stream) {
-  return launch_pdl(chunk_attn_tc_kernel<D, FMT>, dim3(grid), dim3(Cfg<D, FMT>::THREADS), Cfg<D, FMT>::SMEM, stream, map, p);
+  const cudaError_t e = launch_pdl(chunk_attn_tc_kernel<D, FMT>, dim3(grid), dim3(Cfg<D, FMT>::THREADS), Cfg<D, FMT>::SMEM, stream, map, p);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(chunk_join_kernel<D>, dim3(grid, 2 * D / 16), dim3(BM), 0, stream, p);
 }
 
 template <int D, int FMT>
