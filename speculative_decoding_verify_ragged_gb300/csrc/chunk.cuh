@@ -67,6 +67,20 @@ __device__ __forceinline__ int row_sequence(const int* s_off, int B, int r) {
   return lo;
 }
 
+// Cache loads are used once by this SM: kept out of L1.
+__device__ __forceinline__ uint4 load16(const uint4* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint2 load8(const uint2* p) {
+  uint2 v;
+  asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  return v;
+}
+
 // Two e4m3 codes (low byte first) as fp16, exact.
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t x) {
   uint32_t r;

@@ -57,20 +57,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   return r;
 }
 
-// Cache loads are used once by this SM: kept out of L1.
-__device__ __forceinline__ uint4 load16(const uint4* p) {
-  uint4 v;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
-}
-__device__ __forceinline__ uint2 load8(const uint2* p) {
-  uint2 v;
-  asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
-  return v;
-}
-
 template <int D, int FMT>
 __device__ __forceinline__ void load_page(Frag<D, FMT>& f, const ChunkParams& c, int page, int h, int g, int t) {
   using F = Frag<D, FMT>;

@@ -55,7 +55,7 @@ struct Cfg {
   static constexpr int FULL_COUNT = kCodes ? 4 : 1;
   // registers a thread: softmax, products and copies, conversion (launched with
   // 65536 / THREADS, rounded down to a multiple of 8: 168, or 128)
-  static constexpr int R_SOFT = kCodes ? 168 : 192, R_ISSUE = kCodes ? 72 : 120, R_CONV = 104;
+  static constexpr int R_SOFT = kCodes ? 176 : 192, R_ISSUE = kCodes ? 48 : 120, R_CONV = 112;
   static_assert(2 * R_SOFT + R_ISSUE + (kCodes ? R_CONV : 0) <= (kCodes ? 4 * 128 : 3 * 168), "register shares");
   static constexpr int T_O = 2 * BK;                  // TMEM columns of O_0
 };
@@ -232,6 +232,11 @@ struct Part {
   int b, h, qt, b0, b1;
   long long u0;
 };
+// An item whose output is to be taken from TMEM: its rows, the runs [first, last] that hold a
+// part of it, and whether this one had steps.
+struct Held {
+  int off, h, row0, rows, first, last, went;
+};
 struct Place {
   int b, h, qt, blk;
   long long u0;
@@ -262,7 +267,10 @@ __global__ void __launch_bounds__(Cfg<D, FMT>::THREADS, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
   __shared__ long long s_scan[2];  // units of a run; of the launch
   __shared__ Place s_start;
-  __shared__ Part s_part[8];       // the softmax warps' place in the run, out of their registers
+  // the softmax warps' place in the run, and the item whose output is still in
+  // TMEM: out of the registers of their inner loop
+  __shared__ Part s_part[8];
+  __shared__ Held s_held[8];
   __shared__ int s_flag[2][2];     // [tile][turn] whether the others' parts of an item are all there
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -534,65 +542,80 @@ __global__ void __launch_bounds__(Cfg<D, FMT>::THREADS, 1)
           next();
         }
       } else {
-        // 8 lanes (4 with 64 columns) a row, 16 codes each; a row's next codes
-        // are asked for as soon as its last ones are stored
-        constexpr int LANES = D / 16, STEP = 128 / LANES, NR = BK / STEP;
-        const int ct = tid - CONV_WARP * kWarp, ch = ct % LANES, r0 = ct / LANES;
-        uint4 w[NR];
-        uint32_t sc[NR];
-        auto ask = [&](int jj, int kv, int2 rows, int i) {
-          const int r = r0 + i * STEP;
-          const int page = __shfl_sync(0xffffffffu, ids, ((jj & 3) * BPAGES + (r >> 4)) & 31);
-          w[i] = make_uint4(0u, 0u, 0u, 0u);
-          sc[i] = 127;
-          if (r >= rows.x && r < rows.y) {
-            const long long place = (((long long)page * n_kv + h) * 2 + kv) * kPage + (r & 15);
-            w[i] = *reinterpret_cast<const uint4*>(p.c.pool + place * D + ch * 16);
-            sc[i] = p.c.scales[place];
+        // A warp takes two pages of the block's eight: 8 lanes (4 with 64 columns)
+        // a row, 16 codes each.  K and V have registers of their own, asked for
+        // again (for the next block) as soon as they are stored, so two tiles are
+        // on their way at any time; a lane holds the scale of one of the 32 rows.
+        constexpr int LANES = D / 16, RP = kWarp / LANES, NR = kWarp / RP;  // rows a pass, passes
+        const int cw = warp - CONV_WARP, ch = lane % LANES, sub = lane / LANES;
+        const uint32_t page_bytes = static_cast<uint32_t>(n_kv) * 2 * kPage * D, page_scales = static_cast<uint32_t>(n_kv) * 2 * kPage;
+        uint4 w[2][NR];
+        uint32_t sc[2];
+        const uint8_t* from[2];  // this lane's 16 bytes of the first row of the warp's two pages
+        auto ask_rows = [&](int jj, int kv) {  // where block jj's rows are, and their scales
+          const int2 rows = seen(jj);
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const uint32_t page = __shfl_sync(0xffffffffu, ids, ((jj & 3) * BPAGES + 2 * cw + y) & 31);
+            from[y] = p.c.pool + (unsigned long long)page * page_bytes + ((h * 2 + kv) * kPage + sub) * D + ch * 16;
           }
+          const uint32_t page = __shfl_sync(0xffffffffu, ids, ((jj & 3) * BPAGES + 2 * cw + (lane >> 4)) & 31);
+          const int r = cw * kWarp + lane;
+          sc[kv] = 127;
+          if (r >= rows.x && r < rows.y) sc[kv] = p.c.scales[(unsigned long long)page * page_scales + (h * 2 + kv) * kPage + (lane & 15)];
+          return rows;
         };
-        {
-          const int2 rows = seen(0);
+        auto ask = [&](int2 rows, int kv, int i) {
+          const int r = cw * kWarp + i * RP + sub;
+          w[kv][i] = make_uint4(0u, 0u, 0u, 0u);
+          if (r >= rows.x && r < rows.y) w[kv][i] = load16(reinterpret_cast<const uint4*>(from[i * RP >> 4] + (i * RP & 15) * D));
+        };
 #pragma unroll
-          for (int i = 0; i < NR; ++i) ask(0, 0, rows, i);
+        for (int kv = 0; kv < 2; ++kv) {
+          const int2 rows = ask_rows(0, kv);
+#pragma unroll
+          for (int i = 0; i < NR; ++i) ask(rows, kv, i);
         }
-        for (int tile = 0; tile < 2 * n; ++tile) {
-          const int jn = (tile + 1) >> 1, kvn = (tile + 1) & 1;
-          if (kvn == 0 && (jn & 3) == 0) {
+        for (int jj = 0; jj < n; ++jj) {
+          if (((jj + 1) & 3) == 0) {
             ids = ids_next;
-            ids_next = fetch(jn + 4);
+            ids_next = fetch(jj + 5);
           }
-          const int2 rows = jn < n ? seen(jn) : make_int2(0, 0);
-          wait(&empty[slot], phase ^ 1);
-          if (dead) return false;
-          uint8_t* dst = smem + slot * C::SLOT + (ch >> 2) * HALF;
 #pragma unroll
-          for (int i = 0; i < NR; ++i) {
-            const int r = r0 + i * STEP;
+          for (int kv = 0; kv < 2; ++kv) {
+            wait(&empty[slot], phase ^ 1);
+            if (dead) return false;
             // 2^e in fp16, below its normal range for e = -15
-            const int e = static_cast<int>(sc[i]) - 127;
-            const uint32_t bits = e >= -14 ? static_cast<uint32_t>(e + 15) << 10 : 0x200u;
+            const uint32_t bits = sc[kv] == 112 ? 0x200u : (sc[kv] - 112) << 10;
             const uint32_t pair = bits | (bits << 16);
-            const __half2 m = *reinterpret_cast<const __half2*>(&pair);
-            const uint32_t ws[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-            uint32_t o[8];
-#pragma unroll
-            for (int x = 0; x < 8; ++x) {
-              const uint32_t c2 = e4m3x2_to_f16x2(ws[x >> 1] >> (16 * (x & 1)));
-              const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&c2), m);
-              o[x] = *reinterpret_cast<const uint32_t*>(&y);
-            }
+            int2 rows = make_int2(0, 0);
+            if (jj + 1 < n) rows = ask_rows(jj + 1, kv);
+            uint8_t* dst = smem + slot * C::SLOT + (ch >> 2) * HALF;
             const int c0 = (ch & 3) * 2, f = (ch >> 2) & 1;  // upper halves store their second chunk first: no bank meets twice
-            uint8_t* row = dst + r * 128;
-            const uint4 a = make_uint4(o[0], o[1], o[2], o[3]), c = make_uint4(o[4], o[5], o[6], o[7]);
-            *reinterpret_cast<uint4*>(row + (((c0 + f) ^ (r & 7)) << 4)) = f ? c : a;
-            *reinterpret_cast<uint4*>(row + (((c0 + 1 - f) ^ (r & 7)) << 4)) = f ? a : c;
-            ask(jn, kvn, rows, i);
+#pragma unroll
+            for (int i = 0; i < NR; ++i) {
+              const int r = cw * kWarp + i * RP + sub;
+              const uint32_t mb = __shfl_sync(0xffffffffu, pair, i * RP + sub);
+              const __half2 m = *reinterpret_cast<const __half2*>(&mb);
+              const uint32_t ws[4] = {w[kv][i].x, w[kv][i].y, w[kv][i].z, w[kv][i].w};
+              uint32_t o[8];
+#pragma unroll
+              for (int x = 0; x < 8; ++x) {
+                const uint32_t c2 = e4m3x2_to_f16x2(ws[x >> 1] >> (16 * (x & 1)));
+                const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&c2), m);
+                o[x] = *reinterpret_cast<const uint32_t*>(&y);
+              }
+              uint8_t* row = dst + r * 128;
+              const uint4 a = make_uint4(o[0], o[1], o[2], o[3]), c = make_uint4(o[4], o[5], o[6], o[7]);
+              *reinterpret_cast<uint4*>(row + (((c0 + f) ^ (r & 7)) << 4)) = f ? c : a;
+              *reinterpret_cast<uint4*>(row + (((c0 + 1 - f) ^ (r & 7)) << 4)) = f ? a : c;
+              ask(rows, kv, i);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&full[slot]);
+            next();
           }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&full[slot]);
-          next();
         }
       }
       return true;
@@ -708,10 +731,8 @@ __global__ void __launch_bounds__(Cfg<D, FMT>::THREADS, 1)
     };
     // An item's output is taken from TMEM only after the next item's query is on
     // its way, so that the next scores are made meanwhile.
-    bool held = false, in = false, went = false;  // an item whose output is still in TMEM: its row exists; it had steps
+    bool held = false;
     int turn = 0;
-    int c_first = 0, c_last = 0;                  // the blocks that hold a part of it
-    __nv_bfloat16* dst = nullptr;
     float m = kNoMax, l = 0.f;
     for (bool more = true;;) {
       Part part;
@@ -728,23 +749,16 @@ __global__ void __launch_bounds__(Cfg<D, FMT>::THREADS, 1)
       const SeqRows& s = part.s;
       const Item& it = part.it;
       Tile x;
-      x.s0 = x.s1 = 0;
-      bool in_next = false;
-      int row = 0;
+      x.s0 = x.s1 = x.rows = 0;
+      x.pmin = x.pmax = -1;
+      if (more) x = clip(make_tile(s, it, group, window, t), part.b0, part.b1);
+      const int row = it.row0 + t * BM + i;
+      const bool in_next = i < x.rows;
       float cz = p.scale_log2;
-      long long tok = 0;
-      int head = 0;
-      if (more) {
-        const Tile whole = make_tile(s, it, group, window, t);
-        x = clip(whole, part.b0, part.b1);
-        row = it.row0 + t * BM + i;
-        in_next = i < whole.rows;
-        tok = s.off + (in_next ? row / group : 0);
-        head = part.h * group + (in_next ? row % group : 0);
-      }
       if (x.s0 < x.s1 && !dead) {
         // this row's query into the tile (its last readers are done: the scores were all seen)
-        const uint4* src = reinterpret_cast<const uint4*>(p.q + tok * p.q_stride + (long long)head * D);
+        const uint4* src = reinterpret_cast<const uint4*>(
+            p.q + (in_next ? (long long)(s.off + row / group) * p.q_stride + (long long)(part.h * group + row % group) * D : 0));
         uint8_t* q_row = smem + C::OFF_Q + t * C::SLOT + i * 128;
         uint4 w[D / 8];
 #pragma unroll
@@ -778,6 +792,10 @@ __global__ void __launch_bounds__(Cfg<D, FMT>::THREADS, 1)
         if (lane == 0) mbar_arrive(&q_full[t]);
       }
       if (held) {
+        const Held e = s_held[warp];
+        const int c_first = e.first, c_last = e.last, e_row = e.row0 + t * BM + i;
+        const bool went = e.went != 0, in = t * BM + i < e.rows;
+        __nv_bfloat16* dst = p.out + (in ? (long long)(e.off + e_row / group) * p.out_stride + (long long)(e.h * group + e_row % group) * D : 0);
         if (went) {
           wait(&o_full[t], oph);
           oph ^= 1;
@@ -900,27 +918,29 @@ __global__ void __launch_bounds__(Cfg<D, FMT>::THREADS, 1)
         tc_fence_before();
       }
       if (!more) break;
-      in = in_next;
-      went = x.s0 < x.s1;
-      dst = p.out + tok * p.out_stride + (long long)head * D;
-      c_first = static_cast<int>((part.u0 + kItemCost) / per_cta);
-      c_last = static_cast<int>((part.u0 + kItemCost + (long long)(it.blocks - 1) * weight(it)) / per_cta);
-      if (tid == 0 && c_last - c_first > kJoinHere && c_first == (int)blockIdx.x) {
-        p.cuts[2 * blockIdx.x] = make_int4(c_last, s.off, part.h, it.row0);
-        p.cuts[2 * blockIdx.x + 1].x = it.rows;
+      {
+        const int c_first = static_cast<int>((part.u0 + kItemCost) / per_cta);
+        const int c_last = static_cast<int>((part.u0 + kItemCost + (long long)(it.blocks - 1) * weight(it)) / per_cta);
+        __syncwarp();
+        if (lane == 0) s_held[warp] = Held{s.off, part.h, it.row0, it.rows, c_first, c_last, x.s0 < x.s1};
+        if (tid == 0 && c_last - c_first > kJoinHere && c_first == (int)blockIdx.x) {
+          p.cuts[2 * blockIdx.x] = make_int4(c_last, s.off, part.h, it.row0);
+          p.cuts[2 * blockIdx.x + 1].x = it.rows;
+        }
+        __syncwarp();
       }
       m = kNoMax;
       l = 0.f;
-      const int pos = in ? s.pos0 + row / group : -1;
+      // step j holds the keys from key_base + 64 j; steps [cut_lo, cut_hi) are seen whole by every row
+      const int key_base = it.page_lo * kPage, rel_base = (in_next ? s.pos0 + row / group : -1) - key_base;
+      const int cut_hi = (x.pmin - key_base + 1) >> 6;
+      const int cut_lo = window > 0 ? ((x.pmax - window - key_base) >> 6) + 1 : 0;
       for (int j = x.s0; j < x.s1; ++j, ++n) {
         wait(&s_full[2 * t + (n & 1)], (n >> 1) & 1);
         const uint32_t t_sb = t_s + (n & 1) * SK;
-        const int key0 = it.page_lo * kPage + j * SK;
-        // key column c is seen when c <= rel and c > rel - window
-        const bool cut = key0 + SK - 1 > x.pmin || (window > 0 && key0 <= x.pmax - window);
-        const int rel = pos - key0;
+        const int rel = rel_base - j * SK;  // column c is seen when c <= rel and c > rel - window
         uint32_t buf[2][32];
-        if (cut) {
+        if (j >= cut_hi || j < cut_lo) {
           // hide what is not seen, in TMEM, so that what follows is one code for all steps
 #pragma unroll
           for (int c = 0; c < SK / 32; ++c) {
