@@ -218,11 +218,12 @@ __device__ __forceinline__ Tile make_tile(const SeqRows& s, const Item& it, int 
   return x;
 }
 
-// What a block of the item costs: its tiles; and an item before its first block
-// (query, first scores, output: about two blocks' time, which without it left
-// the SMs with the short items at the end: 4096 new tokens 193 -> 136 us).
-__device__ __forceinline__ int weight(const Item& it) { return it.rows > BM ? 2 : 1; }
-constexpr int kItemCost = 6;
+// What a block of the item costs, and an item before its first block (query,
+// first scores, output), in eighths of a block of two tiles: measured, a block
+// of one tile takes 2450 cycles against 2750 and an item begins at 3.7 blocks.
+// (With every block alike the SMs with the short items ended last: 4096 new tokens 193 us.)
+__device__ __forceinline__ int weight(const Item& it) { return it.rows > BM ? 8 : 7; }
+constexpr int kItemCost = 28;
 __device__ __forceinline__ int units_of(const Item& it) { return kItemCost + it.blocks * weight(it); }
 
 // A part of a run: blocks [b0, b1) of an item of (sequence b, key head h) whose first unit is u0.
@@ -351,7 +352,7 @@ __global__ void __launch_bounds__(Cfg<D, FMT>::THREADS, 1)
         for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
         total += v;
       }
-      const long long per = max(2LL, (total + gridDim.x - 1) / gridDim.x);  // two: a block of two tiles begins in every run
+      const long long per = max(8LL, (total + gridDim.x - 1) / gridDim.x);  // eight: a block begins in every run that an item spans
       const long long u = (long long)blockIdx.x * per;
       if (u < total) {
         long long base = 0;
@@ -757,36 +758,40 @@ __global__ void __launch_bounds__(Cfg<D, FMT>::THREADS, 1)
       float cz = p.scale_log2;
       if (x.s0 < x.s1 && !dead) {
         // this row's query into the tile (its last readers are done: the scores were all seen)
-        const uint4* src = reinterpret_cast<const uint4*>(
-            p.q + (in_next ? (long long)(s.off + row / group) * p.q_stride + (long long)(part.h * group + row % group) * D : 0));
-        uint8_t* q_row = smem + C::OFF_Q + t * C::SLOT + i * 128;
-        uint4 w[D / 8];
+        // the warp's 32 rows, D / 8 lanes a row
+        constexpr int QL = D / 8, QR = kWarp / QL;  // lanes a row, rows a pass
+        const long long mine = in_next ? (long long)(s.off + row / group) * p.q_stride + (long long)(part.h * group + row % group) * D : -1;
+        const int ch = lane % QL, sub = lane / QL;
+        uint8_t* q_rows = smem + C::OFF_Q + t * C::SLOT + (ch >> 3) * HALF + (i & ~31) * 128;
+        uint4 w[QL];
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) w[c] = in_next ? src[c] : make_uint4(0u, 0u, 0u, 0u);
-        if constexpr (C::kCodes) {
-          // fp16 with the row's largest magnitude in [1/2, 1)
-          float a = 0.f;
-#pragma unroll
-          for (int c = 0; c < D / 8; ++c) {
-            const uint32_t* v = &w[c].x;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) a = fmaxf(a, fmaxf(fabsf(__uint_as_float(v[k] << 16)), fabsf(__uint_as_float(v[k] & 0xFFFF0000u))));
-          }
-          const int e = min(max(static_cast<int>(__float_as_uint(a) >> 23) - 126, -100), 100);
-          const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-          cz *= __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-#pragma unroll
-          for (int c = 0; c < D / 8; ++c) {
-            uint32_t* v = &w[c].x;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const __half2 y = __floats2half2_rn(__uint_as_float(v[k] << 16) * inv, __uint_as_float(v[k] & 0xFFFF0000u) * inv);
-              v[k] = *reinterpret_cast<const uint32_t*>(&y);
-            }
-          }
+        for (int k = 0; k < QL; ++k) {
+          const long long at = __shfl_sync(0xffffffffu, mine, k * QR + sub);
+          w[k] = at >= 0 ? *reinterpret_cast<const uint4*>(p.q + at + ch * 8) : make_uint4(0u, 0u, 0u, 0u);
         }
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) *reinterpret_cast<uint4*>(q_row + (c >> 3) * HALF + (((c & 7) ^ (i & 7)) << 4)) = w[c];
+        for (int k = 0; k < QL; ++k) {
+          if constexpr (C::kCodes) {
+            // fp16 with the row's largest magnitude in [1/2, 1)
+            uint32_t* v = &w[k].x;
+            float a = 0.f;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) a = fmaxf(a, fmaxf(fabsf(__uint_as_float(v[x] << 16)), fabsf(__uint_as_float(v[x] & 0xFFFF0000u))));
+#pragma unroll
+            for (int d = 1; d < QL; d <<= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, d));
+            const int e = min(max(static_cast<int>(__float_as_uint(a) >> 23) - 126, -100), 100);
+            const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const __half2 y = __floats2half2_rn(__uint_as_float(v[x] << 16) * inv, __uint_as_float(v[x] & 0xFFFF0000u) * inv);
+              v[x] = *reinterpret_cast<const uint32_t*>(&y);
+            }
+            const int er = __shfl_sync(0xffffffffu, e, (lane % QR) * QL);  // the exponent of row k QR + lane % QR
+            if (lane / QR == k) cz = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + er) << 23);
+          }
+          const int r = k * QR + sub;
+          *reinterpret_cast<uint4*>(q_rows + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = w[k];
+        }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&q_full[t]);
@@ -795,7 +800,6 @@ __global__ void __launch_bounds__(Cfg<D, FMT>::THREADS, 1)
         const Held e = s_held[warp];
         const int c_first = e.first, c_last = e.last, e_row = e.row0 + t * BM + i;
         const bool went = e.went != 0, in = t * BM + i < e.rows;
-        __nv_bfloat16* dst = p.out + (in ? (long long)(e.off + e_row / group) * p.out_stride + (long long)(e.h * group + e_row % group) * D : 0);
         if (went) {
           wait(&o_full[t], oph);
           oph ^= 1;
@@ -811,7 +815,7 @@ __global__ void __launch_bounds__(Cfg<D, FMT>::THREADS, 1)
           join = others <= kJoinHere;
           int* count = p.counters + 2 * c_first + t;
           bool last = false;
-          if (join) {
+          if (join && c_first == (int)blockIdx.x) {
             turn ^= 1;
             if (i == 0) {
               s_flag[t][turn] = atomicAdd(count, 0) == others;
@@ -874,6 +878,7 @@ __global__ void __launch_bounds__(Cfg<D, FMT>::THREADS, 1)
           }
         }
         const float inv = l == 0.f ? 0.f : 1.f / l;  // a row that sees nothing gives 0
+        const long long out_at = write ? (long long)(e.off + e_row / group) * p.out_stride + (long long)(e.h * group + e_row % group) * D : -1;
         if (others == 0 || __any_sync(0xffffffffu, join && write)) {
 #pragma unroll
           for (int c = 0; c < D / 32; ++c) {
@@ -904,15 +909,34 @@ __global__ void __launch_bounds__(Cfg<D, FMT>::THREADS, 1)
 #pragma unroll
               for (int x = 0; x < 32; ++x) r[x] = __float_as_uint(acc[x]);
             }
-            if (write)
+            // the 32 columns as four pieces of 16 bytes; four lanes trade theirs, so
+            // that they store one row's 64 bytes together
+            uint32_t o[4][4];
 #pragma unroll
-              for (int k = 0; k < 32; k += 8) {
-                uint32_t o[4];
+            for (int k = 0; k < 4; ++k)
 #pragma unroll
-                for (int y = 0; y < 4; ++y)
-                  o[y] = l == 0.f ? 0u : pack_bf16x2(__uint_as_float(r[k + 2 * y]) * inv, __uint_as_float(r[k + 2 * y + 1]) * inv);
-                *reinterpret_cast<uint4*>(dst + 32 * c + k) = make_uint4(o[0], o[1], o[2], o[3]);
+              for (int y = 0; y < 4; ++y)
+                o[k][y] = l == 0.f ? 0u : pack_bf16x2(__uint_as_float(r[8 * k + 2 * y]) * inv, __uint_as_float(r[8 * k + 2 * y + 1]) * inv);
+#pragma unroll
+            for (int bit = 1; bit <= 2; bit <<= 1) {
+              const bool up = lane & bit;
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                if (k & bit) continue;
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                  const uint32_t give = up ? o[k][y] : o[k | bit][y];
+                  const uint32_t got = __shfl_xor_sync(0xffffffffu, give, bit);
+                  if (up) o[k][y] = got;
+                  else o[k | bit][y] = got;
+                }
               }
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {  // o[k] is piece lane % 4 of row lane & ~3 + k
+              const long long at = __shfl_sync(0xffffffffu, out_at, (lane & ~3) + k);
+              if (at >= 0) *reinterpret_cast<uint4*>(p.out + at + 32 * c + (lane & 3) * 8) = make_uint4(o[k][0], o[k][1], o[k][2], o[k][3]);
+            }
           }
         }
         tc_fence_before();
