@@ -108,7 +108,7 @@ extern "C" sdv_status sdv_cache_create(const sdv_cache_config* cfg, void* worksp
   if (!config_ok(cfg) || !workspace || max_rows <= 0 || max_slots <= 0 || (reinterpret_cast<uintptr_t>(workspace) & 255))
     return SDV_ERR_INVALID_ARG;
   if (!shape_ok(cfg)) return SDV_ERR_UNSUPPORTED;
-  if (max_slots > kMaxChunkSlots || (long long)max_rows * cfg->n_q > 0x7FFFFFFFLL) return SDV_ERR_CAPACITY;
+  if (max_slots > kMaxChunkSlots || (long long)max_rows * cfg->n_q > 0x3FFFFFFFLL) return SDV_ERR_CAPACITY;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return cuda_fail(e);

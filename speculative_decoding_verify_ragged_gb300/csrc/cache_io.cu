@@ -5,17 +5,43 @@ namespace sdv {
 namespace {
 
 constexpr int IO_THREADS = 256;
+constexpr int READ_BLOCKS = 8;  // blocks per SM (3, 4, 6 and 8: 45.9, 44.0, 44.4 and 42.6 us for 32749 bf16 rows)
 
-// 4 consecutive elements as fp32.
-__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
-__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
-  const uint2 w = *reinterpret_cast<const uint2*>(p);
-  return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u), __uint_as_float(w.y << 16),
-                     __uint_as_float(w.y & 0xFFFF0000u));
+// 8 or 4 consecutive elements as fp32, in one 16-byte load.
+__device__ __forceinline__ void load_elements(const float* p, float (&x)[4]) {
+  const float4 w = *reinterpret_cast<const float4*>(p);
+  x[0] = w.x, x[1] = w.y, x[2] = w.z, x[3] = w.w;
+}
+__device__ __forceinline__ void load_elements(const __nv_bfloat16* p, float (&x)[8]) {
+  const uint4 w = *reinterpret_cast<const uint4*>(p);
+  const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    x[2 * j] = __uint_as_float(ws[j] << 16);
+    x[2 * j + 1] = __uint_as_float(ws[j] & 0xFFFF0000u);
+  }
 }
 
-__device__ __forceinline__ float max_abs(float m, const float4& a) {  // fmaxf drops NaNs
-  return fmaxf(fmaxf(fmaxf(m, fabsf(a.x)), fmaxf(fabsf(a.y), fabsf(a.z))), fabsf(a.w));
+template <int N>
+__device__ __forceinline__ void store_bf16(__nv_bfloat16* p, const float (&x)[N]) {
+  uint32_t w[N / 2];
+#pragma unroll
+  for (int j = 0; j < N / 2; ++j) w[j] = pack_bf16x2(x[2 * j], x[2 * j + 1]);
+  if constexpr (N == 8) *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  else *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+}
+
+template <int N>
+__device__ __forceinline__ void store_codes(uint8_t* p, const float (&x)[N], float inv) {
+  uint32_t w[N / 4];
+#pragma unroll
+  for (int j = 0; j < N / 4; ++j) {
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(x[4 * j] * inv, x[4 * j + 1] * inv), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(x[4 * j + 2] * inv, x[4 * j + 3] * inv), __NV_SATFINITE, __NV_E4M3);
+    w[j] = lo | (hi << 16);
+  }
+  if constexpr (N == 8) *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+  else *reinterpret_cast<uint32_t*>(p) = w[0];
 }
 
 // Smallest e in [kScaleMin, kScaleMax] with amax <= 448 * 2^e: with amax = m 2^x
@@ -26,200 +52,256 @@ __device__ __forceinline__ int scale_exponent(float amax) {
   return min(max(x - 8 + ((b & 0x7FFFFFu) > 0x600000u ? 1 : 0), kScaleMin), kScaleMax);
 }
 
-__device__ __forceinline__ uint32_t codes4(const float4& a, float inv) {
-  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a.x * inv, a.y * inv), __NV_SATFINITE, __NV_E4M3);
-  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(a.z * inv, a.w * inv), __NV_SATFINITE, __NV_E4M3);
-  return lo | (hi << 16);
+// Where row r of the chunk lives: its position (below 0: nowhere) and that
+// position's page (-1: a bad page id, reported here).
+__device__ __forceinline__ int2 row_place(const ChunkParams& c, const int* s_off, const int* s_len, int r) {
+  const int b = row_sequence(s_off, c.B, r);
+  const int pos = s_len[b] - s_off[b + 1] + r;
+  if (pos < 0) return make_int2(pos, -1);
+  int page = c.page_table[(long long)b * c.max_pages + pos / kPage];
+  if (page < 0 || page >= c.pool_pages) {
+    set_status(c.status, SDV_ERR_PAGE_RANGE);
+    page = -1;
+  }
+  return make_int2(pos, page);
 }
 
-// One block takes rows of the chunk in turn; D / 8 lanes take one head of the
-// row, each lane 4 elements of its lower half and the 4 that the rotation pairs
-// them with in its upper half, so the rotation and the row maximum stay in
-// registers and every input is read once.
+// A block takes `per` rows of the chunk at a time; a few lanes take one head of
+// a row, each with the elements that the rotation pairs in both halves, so that
+// rotation and row maximum stay in registers and every input is read once, in 16-byte
+// loads, several heads' at a time.  The next rows' places, cosines and sines are
+// made while these rows' data travels: one barrier a round.
 //
 // Angles: position * theta^(-2j/d) in turns is a product of integers modulo 2^64
 // (RopeTurns), so far positions lose nothing; the quarter turns are taken off
-// as integers before the rest is rounded to fp32.  Each row's cosines and
-// sines are computed once for all its heads.
+// as integers before the rest is rounded to fp32.
+//
+// Bound by the input's bytes.  8192 rows of 48 heads of 128, fp32 to e4m3 and
+// queries to bf16 (285 MB): 48.4 us, 5.9 TB/s.
 template <int D, int FMT, typename T>
 __global__ void __launch_bounds__(IO_THREADS)
-    cache_append_kernel(const AppendParams p, const __grid_constant__ RopeTurns turns) {
+    cache_append_kernel(const AppendParams p, const __grid_constant__ RopeTurns turns, int per) {
   extern __shared__ int s_meta[];
-  __shared__ float2 s_cs[2][D / 2];
-  constexpr int LANES = D / 8;
-  constexpr int GROUPS = IO_THREADS / LANES;
+  constexpr int PAIRS = D / 2, ROWS = IO_THREADS / PAIRS;  // rows a round at most
+  constexpr int N = 16 / sizeof(T), LANES = PAIRS / N, GROUPS = IO_THREADS / LANES;
+  constexpr int AHEAD = sizeof(T) == 4 ? 4 : 2;            // heads a group has on their way
+  __shared__ float2 s_cs[2][ROWS][PAIRS];
+  __shared__ int2 s_place[2][ROWS];
   griddep_launch_dependents();
   griddep_wait();
-  if (read_status(p.c.status) != 0) return;
+  bool dead;
   int* s_off = s_meta;
   int* s_len = s_meta + p.c.B + 1;
-  if (!load_chunk(p.c, s_off, s_len)) return;
+  if (!load_chunk(p.c, s_off, s_len, dead) || dead) return;
   const int rows = s_off[p.c.B];
   const int n_kv = p.c.n_kv, heads = 2 * n_kv + (p.q_out ? p.c.n_q : 0);
-  const int group = threadIdx.x / LANES, lane = threadIdx.x % LANES;
-  const unsigned long long turn = turns.f[threadIdx.x % (D / 2)];
-  const unsigned mask = LANES == 16 ? 0xFFFFu << (threadIdx.x & 16) : 0xFFu << (threadIdx.x & 24);
+  const int tid = threadIdx.x, group = tid / LANES, lane = tid % LANES;
+  const unsigned long long turn = turns.f[tid % PAIRS];
+  const unsigned mask = LANES == 32 ? 0xFFFFFFFFu : ((1u << LANES) - 1) << ((tid & 31) / LANES * LANES);
+  auto prepare = [&](int r0, int buf) {
+    const int k = tid / PAIRS;
+    if (p.rope && k < per && r0 + k < rows) {
+      const int b = row_sequence(s_off, p.c.B, r0 + k);
+      const int pos = s_len[b] - s_off[b + 1] + r0 + k;  // (of a row below 0 nothing is used)
+      const uint32_t t = static_cast<uint32_t>((turn * static_cast<unsigned long long>(max(pos, 0))) >> 32);
+      const uint32_t quarter = (t + (1u << 29)) >> 30;
+      const float x = static_cast<float>(static_cast<int>(t - (quarter << 30))) * 0x1p-31f;  // half turns, |x| <= 1/4
+      float s, c;
+      sincospif(x, &s, &c);
+      const float sw = (quarter & 1) ? s : c;  // cos of the whole angle up to sign
+      const float tw = (quarter & 1) ? c : s;
+      s_cs[buf][k][tid % PAIRS] = make_float2(((quarter + 1) & 2) ? -sw : sw, (quarter & 2) ? -tw : tw);
+    }
+    if (tid < per && r0 + tid < rows) s_place[buf][tid] = row_place(p.c, s_off, s_len, r0 + tid);
+  };
+  const int step = gridDim.x * per;
   int buf = 0;
-  for (int r = blockIdx.x; r < rows; r += gridDim.x) {
-    const int b = row_sequence(s_off, p.c.B, r);
-    const int pos = s_len[b] - s_off[b + 1] + r;
-    if (pos < 0) continue;  // the same for the whole block
-    if (p.rope) {
-      if (threadIdx.x < D / 2) {
-        const uint32_t t = static_cast<uint32_t>((turn * static_cast<unsigned long long>(pos)) >> 32);
-        const uint32_t quarter = (t + (1u << 29)) >> 30;
-        const float x = static_cast<float>(static_cast<int>(t - (quarter << 30))) * 0x1p-31f;  // half turns, |x| <= 1/4
-        float s, c;
-        sincospif(x, &s, &c);
-        const float sw = (quarter & 1) ? s : c;  // cos of the whole angle up to sign
-        const float tw = (quarter & 1) ? c : s;
-        s_cs[buf][threadIdx.x] = make_float2(((quarter + 1) & 2) ? -sw : sw, (quarter & 2) ? -tw : tw);
-      }
-      __syncthreads();
-    }
-    int page = -1;
-    for (int h = blockIdx.y * GROUPS + group; h < heads; h += GROUPS * gridDim.y) {
-      const int which = h < n_kv ? 0 : h < 2 * n_kv ? 1 : 2;  // key, value, query
-      const int hh = h - which * n_kv;
-      const T* src = reinterpret_cast<const T*>(which == 0 ? p.k : which == 1 ? p.v : p.q) +
-                     (long long)r * (which == 0 ? p.k_stride : which == 1 ? p.v_stride : p.q_stride) + hh * D + lane * 4;
-      float4 lo = load4(src), hi = load4(src + D / 2);
-      if (p.rope && which != 1) {
-        float* l = &lo.x;
-        float* u = &hi.x;
+  if (blockIdx.x * per < rows) prepare(blockIdx.x * per, 0);
+  __syncthreads();
+  for (int r0 = blockIdx.x * per; r0 < rows; r0 += step, buf ^= 1) {
+    const int items = min(per, rows - r0) * heads;
+    bool made = false;
+    for (int i0 = blockIdx.y * GROUPS + group; i0 < items || !made; i0 += AHEAD * GROUPS * gridDim.y) {
+      float lo[AHEAD][N], hi[AHEAD][N];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 cs = s_cs[buf][lane * 4 + j];
-          const float a = l[j], c = u[j];
-          l[j] = a * cs.x - c * cs.y;
-          u[j] = c * cs.x + a * cs.y;
+      for (int u = 0; u < AHEAD; ++u) {
+        const int i = i0 + u * GROUPS * gridDim.y;
+        if (i < items) {
+          const int k = i / heads, h = i - k * heads, which = h < n_kv ? 0 : h < 2 * n_kv ? 1 : 2;  // key, value, query
+          const T* src = reinterpret_cast<const T*>(which == 0 ? p.k : which == 1 ? p.v : p.q) +
+                         (long long)(r0 + k) * (which == 0 ? p.k_stride : which == 1 ? p.v_stride : p.q_stride) +
+                         (h - which * n_kv) * D + lane * N;
+          load_elements(src, lo[u]);
+          load_elements(src + PAIRS, hi[u]);
         }
       }
-      if (which == 2) {
-        __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(p.q_out) + (long long)r * p.q_out_stride + hh * D + lane * 4;
-        *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(lo.x, lo.y), pack_bf16x2(lo.z, lo.w));
-        *reinterpret_cast<uint2*>(dst + D / 2) = make_uint2(pack_bf16x2(hi.x, hi.y), pack_bf16x2(hi.z, hi.w));
-        continue;
+      if (!made) {
+        made = true;
+        if (r0 + step < rows) prepare(r0 + step, buf ^ 1);
       }
-      if (page < 0) {
-        page = p.c.page_table[(long long)b * p.c.max_pages + pos / kPage];
-        if (page < 0 || page >= p.c.pool_pages) {
-          set_status(p.c.status, SDV_ERR_PAGE_RANGE);
-          page = -1;
+#pragma unroll
+      for (int u = 0; u < AHEAD; ++u) {
+        const int i = i0 + u * GROUPS * gridDim.y;
+        if (i >= items) continue;
+        const int k = i / heads, h = i - k * heads, which = h < n_kv ? 0 : h < 2 * n_kv ? 1 : 2, hh = h - which * n_kv;
+        const int2 at = s_place[buf][k];
+        if (at.x < 0) continue;
+        if (p.rope && which != 1) {
+#pragma unroll
+          for (int j = 0; j < N; ++j) {
+            const float2 cs = s_cs[buf][k][lane * N + j];
+            const float a = lo[u][j], c = hi[u][j];
+            lo[u][j] = a * cs.x - c * cs.y;
+            hi[u][j] = c * cs.x + a * cs.y;
+          }
+        }
+        if (which == 2) {
+          __nv_bfloat16* dst =
+              reinterpret_cast<__nv_bfloat16*>(p.q_out) + (long long)(r0 + k) * p.q_out_stride + hh * D + lane * N;
+          store_bf16(dst, lo[u]);
+          store_bf16(dst + PAIRS, hi[u]);
+          continue;
+        }
+        if (at.y < 0) continue;
+        const long long place = (((long long)at.y * n_kv + hh) * 2 + which) * kPage + at.x % kPage;
+        if constexpr (FMT == SDV_CACHE_BF16) {
+          __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(p.c.pool) + place * D + lane * N;
+          store_bf16(dst, lo[u]);
+          store_bf16(dst + PAIRS, hi[u]);
+        } else {
+          float m = 0.f;  // fmaxf drops NaNs
+#pragma unroll
+          for (int j = 0; j < N; ++j) m = fmaxf(m, fmaxf(fabsf(lo[u][j]), fabsf(hi[u][j])));
+#pragma unroll
+          for (int o = LANES / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(mask, m, o));
+          const int e = scale_exponent(m);
+          const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);  // 2^-e
+          uint8_t* dst = p.c.pool + place * D + lane * N;
+          store_codes(dst, lo[u], inv);
+          store_codes(dst + PAIRS, hi[u], inv);
+          if (lane == 0) p.c.scales[place] = static_cast<uint8_t>(e + 127);
         }
       }
-      const long long place = (((long long)page * n_kv + hh) * 2 + which) * kPage + pos % kPage;
-      if constexpr (FMT == SDV_CACHE_BF16) {
-        if (page < 0) continue;
-        __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(p.c.pool) + place * D + lane * 4;
-        *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(lo.x, lo.y), pack_bf16x2(lo.z, lo.w));
-        *reinterpret_cast<uint2*>(dst + D / 2) = make_uint2(pack_bf16x2(hi.x, hi.y), pack_bf16x2(hi.z, hi.w));
-      } else {
-        float m = max_abs(max_abs(0.f, lo), hi);
-#pragma unroll
-        for (int o = LANES / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(mask, m, o));
-        const int e = scale_exponent(m);
-        const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);  // 2^-e
-        if (page < 0) continue;
-        uint8_t* dst = p.c.pool + place * D + lane * 4;
-        *reinterpret_cast<uint32_t*>(dst) = codes4(lo, inv);
-        *reinterpret_cast<uint32_t*>(dst + D / 2) = codes4(hi, inv);
-        if (lane == 0) p.c.scales[place] = static_cast<uint8_t>(e + 127);
-      }
     }
-    buf ^= 1;
+    __syncthreads();
   }
 }
 
-// Each group of lanes copies one (row, head, key or value): 16 bytes of codes
-// or 16-bit values a lane.
+// A warp takes a row (of few rows several take one), a lane 16 bytes of codes or
+// 16-bit values of one of its heads, eight at a time; the next row's place is found meanwhile.  Bound by
+// the bytes: 32749 positions of 8 heads of 128, bf16 (268 MB), 42.6 us, 6.3 TB/s.
 template <int D, int FMT, int OUT>
-__global__ void __launch_bounds__(IO_THREADS) cache_read_kernel(const ReadParams p) {
+__global__ void __launch_bounds__(IO_THREADS) cache_read_kernel(const ReadParams p, int split) {
   extern __shared__ int s_meta[];
   constexpr int PER = FMT == SDV_CACHE_BF16 ? 8 : 16;  // elements a lane takes
-  constexpr int LANES = D / PER;
+  constexpr int LANES = D / PER, AHEAD = 8;
   griddep_launch_dependents();
   griddep_wait();
-  if (read_status(p.c.status) != 0) return;
+  bool dead;
   int* s_off = s_meta;
   int* s_len = s_meta + p.c.B + 1;
-  if (!load_chunk(p.c, s_off, s_len)) return;
-  const int n_kv = p.c.n_kv;
-  const long long total = (long long)s_off[p.c.B] * n_kv * 2;
-  const int lane = threadIdx.x % LANES;
-  const long long step = (long long)gridDim.x * (IO_THREADS / LANES);
-  for (long long i = (long long)blockIdx.x * (IO_THREADS / LANES) + threadIdx.x / LANES; i < total; i += step) {
-    const int r = static_cast<int>(i / (2 * n_kv)), hw = static_cast<int>(i - (long long)r * 2 * n_kv);
-    const int which = hw >= n_kv, h = hw - which * n_kv;
-    void* base = which ? p.v : p.k;
-    if (!base) continue;
-    const int b = row_sequence(s_off, p.c.B, r);
-    const int pos = s_len[b] - s_off[b + 1] + r;
-    float x[PER];
-#pragma unroll
-    for (int j = 0; j < PER; ++j) x[j] = 0.f;
-    if (pos >= 0) {
-      const int page = p.c.page_table[(long long)b * p.c.max_pages + pos / kPage];
-      if (page < 0 || page >= p.c.pool_pages) {
-        set_status(p.c.status, SDV_ERR_PAGE_RANGE);
-        continue;
-      }
-      const long long place = (((long long)page * n_kv + h) * 2 + which) * kPage + pos % kPage;
-      if constexpr (FMT == SDV_CACHE_BF16) {
-        const uint4 w = *reinterpret_cast<const uint4*>(p.c.pool + (place * D + lane * PER) * 2);
-        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          x[2 * j] = __uint_as_float(ws[j] << 16);
-          x[2 * j + 1] = __uint_as_float(ws[j] & 0xFFFF0000u);
-        }
-      } else {
-        const uint4 w = *reinterpret_cast<const uint4*>(p.c.pool + place * D + lane * PER);
-        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-        const float s = scale_value(p.c.scales[place]);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const uint32_t h2 = e4m3x2_to_f16x2(ws[j >> 1] >> (16 * (j & 1)));
-          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
-          x[2 * j] = f.x * s;
-          x[2 * j + 1] = f.y * s;
-        }
-      }
+  if (!load_chunk(p.c, s_off, s_len, dead) || dead) return;
+  // the heads asked for: keys, values or both
+  const int n_kv = p.c.n_kv, first = p.k ? 0 : n_kv, pieces = ((p.v ? 2 * n_kv : n_kv) - first) * LANES;
+  const int rows = s_off[p.c.B], wid = blockIdx.x * (IO_THREADS / kWarp) + (threadIdx.x >> 5);
+  const int lane = (threadIdx.x & 31) + wid % split * kWarp, lanes = split * kWarp;  // of the row's
+  const int warps = gridDim.x * (IO_THREADS / kWarp) / split;
+  int r = wid / split;
+  int2 next = r < rows ? row_place(p.c, s_off, s_len, r) : make_int2(-1, -1);
+  for (; r < rows; r += warps) {
+    const int2 at = next;
+    const bool there = at.y >= 0;
+    if (at.x >= 0 && !there) {  // a bad page id: reported, nothing written
+      if (r + warps < rows) next = row_place(p.c, s_off, s_len, r + warps);
+      continue;
     }
-    const long long at = (long long)r * (which ? p.v_stride : p.k_stride) + h * D + lane * PER;
-    if constexpr (OUT == 0) {
-      uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(base) + at);
+    const long long base = ((long long)(there ? at.y : 0) * n_kv * 2) * kPage + at.x % kPage;  // + (2 h + which) * 16
+    for (int j0 = lane; j0 < pieces || j0 == lane; j0 += AHEAD * lanes) {
+      uint4 w[AHEAD];
+      float s[AHEAD];
 #pragma unroll
-      for (int j = 0; j < PER; j += 8)
-        dst[j / 8] = make_uint4(pack_bf16x2(x[j], x[j + 1]), pack_bf16x2(x[j + 2], x[j + 3]), pack_bf16x2(x[j + 4], x[j + 5]),
-                                pack_bf16x2(x[j + 6], x[j + 7]));
-    } else {
-      float4* dst = reinterpret_cast<float4*>(reinterpret_cast<float*>(base) + at);
+      for (int u = 0; u < AHEAD; ++u) {
+        const int j = j0 + u * lanes, hw = first + j / LANES, which = hw >= n_kv, h = hw - which * n_kv;
+        w[u] = make_uint4(0u, 0u, 0u, 0u);
+        s[u] = 0.f;
+        if (there && j < pieces) {
+          const long long place = base + (2 * h + which) * kPage;
+          w[u] = *reinterpret_cast<const uint4*>(p.c.pool + (place * D + j % LANES * PER) * (FMT == SDV_CACHE_BF16 ? 2 : 1));
+          if constexpr (FMT == SDV_CACHE_E4M3) s[u] = scale_value(p.c.scales[place]);
+        }
+      }
+      if (j0 == lane && r + warps < rows) next = row_place(p.c, s_off, s_len, r + warps);
 #pragma unroll
-      for (int j = 0; j < PER; j += 4) dst[j / 4] = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
+      for (int u = 0; u < AHEAD; ++u) {
+        const int j = j0 + u * lanes, hw = first + j / LANES, which = hw >= n_kv, h = hw - which * n_kv;
+        if (j >= pieces) continue;
+        const uint32_t ws[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+        const long long to = (long long)r * (which ? p.v_stride : p.k_stride) + h * D + j % LANES * PER;
+        void* out = which ? p.v : p.k;
+        if constexpr (FMT == SDV_CACHE_BF16 && OUT == 0) {
+          *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(out) + to) = w[u];
+        } else {
+          float x[PER];
+          if constexpr (FMT == SDV_CACHE_BF16) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              x[2 * e] = __uint_as_float(ws[e] << 16);
+              x[2 * e + 1] = __uint_as_float(ws[e] & 0xFFFF0000u);
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const uint32_t h2 = e4m3x2_to_f16x2(ws[e >> 1] >> (16 * (e & 1)));
+              const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
+              x[2 * e] = f.x * s[u];
+              x[2 * e + 1] = f.y * s[u];
+            }
+          }
+          if constexpr (OUT == 0) {
+            uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(out) + to);
+#pragma unroll
+            for (int e = 0; e < PER; e += 8)
+              dst[e / 8] = make_uint4(pack_bf16x2(x[e], x[e + 1]), pack_bf16x2(x[e + 2], x[e + 3]),
+                                      pack_bf16x2(x[e + 4], x[e + 5]), pack_bf16x2(x[e + 6], x[e + 7]));
+          } else {
+            float4* dst = reinterpret_cast<float4*>(reinterpret_cast<float*>(out) + to);
+#pragma unroll
+            for (int e = 0; e < PER; e += 4) dst[e / 4] = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+          }
+        }
+      }
     }
   }
 }
 
 size_t meta_bytes(int B) { return static_cast<size_t>(2 * B + 1) * sizeof(int); }
 
+// Rows a block takes at a time: as many as leave every SM several blocks.
+int rows_at_a_time(int T, int most, int blocks) {
+  int per = 1;
+  while (per < most && (T + 2 * per - 1) / (2 * per) >= blocks) per *= 2;
+  return per;
+}
+
 template <int D, int FMT, typename T>
 cudaError_t append_launch(const AppendParams& p, const RopeTurns& turns, int sms, cudaStream_t stream) {
-  constexpr int GROUPS = IO_THREADS / (D / 8);
+  constexpr int GROUPS = IO_THREADS / (D / 2 / (16 / static_cast<int>(sizeof(T))));
   const int heads = 2 * p.c.n_kv + (p.q_out ? p.c.n_q : 0), passes = (heads + GROUPS - 1) / GROUPS;
+  const int per = rows_at_a_time(p.c.T, IO_THREADS / (D / 2), sms * 4);
   // few rows: the heads of a row are spread over blocks as well
-  const int y = (long long)p.c.T * passes <= sms * 8 ? passes : 1;
-  const int x = p.c.T < sms * 8 ? p.c.T : sms * 8;
-  return launch_pdl(cache_append_kernel<D, FMT, T>, dim3(x, y), dim3(IO_THREADS), meta_bytes(p.c.B), stream, p, turns);
+  const int y = (long long)p.c.T * passes <= sms * 4 ? passes : 1;
+  const int want = (p.c.T + per - 1) / per, x = want < sms * 8 ? want : sms * 8;
+  return launch_pdl(cache_append_kernel<D, FMT, T>, dim3(x, y), dim3(IO_THREADS), meta_bytes(p.c.B), stream, p, turns, per);
 }
 
 template <int D, int FMT, int OUT>
 cudaError_t read_launch(const ReadParams& p, int sms, cudaStream_t stream) {
-  constexpr int PER = FMT == SDV_CACHE_BF16 ? 8 : 16;
-  const long long groups = (long long)p.c.T * p.c.n_kv * 2 * (D / PER);
-  const long long want = (groups + IO_THREADS - 1) / IO_THREADS;
-  const int grid = want < sms * 8 ? static_cast<int>(want) : sms * 8;
-  return launch_pdl(cache_read_kernel<D, FMT, OUT>, dim3(grid), dim3(IO_THREADS), meta_bytes(p.c.B), stream, p);
+  constexpr int WARPS = IO_THREADS / kWarp;
+  int split = 1;  // a divisor of the warps of a block
+  while (split < WARPS && (long long)p.c.T * split < sms * WARPS * 2) split *= 2;
+  const long long want = ((long long)p.c.T * split + WARPS - 1) / WARPS;
+  const int grid = want < sms * READ_BLOCKS ? static_cast<int>(want) : sms * READ_BLOCKS;
+  return launch_pdl(cache_read_kernel<D, FMT, OUT>, dim3(grid), dim3(IO_THREADS), meta_bytes(p.c.B), stream, p, split);
 }
 
 }  // namespace

@@ -35,9 +35,12 @@ struct SeqRows {
 
 // Copy offsets [B + 1] and lengths [B] to shared memory and check them.  Every
 // block of a launch reads the same words and comes to the same verdict, so a
-// bad chunk stops all of them before any output.  Ends with a barrier.
-__device__ __forceinline__ bool load_chunk(const ChunkParams& p, int* s_off, int* s_len) {
+// bad chunk stops all of them before any output.  `dead`: the status word was
+// set already; another block may set it meanwhile, so the block's threads agree
+// on what they saw.  Ends with a barrier.
+__device__ __forceinline__ bool load_chunk(const ChunkParams& p, int* s_off, int* s_len, bool& dead) {
   int bad = 0;
+  const int status = read_status(p.status);
   for (int b = threadIdx.x; b < p.B; b += blockDim.x) {
     const int o = p.row_offsets[b], e = p.row_offsets[b + 1], len = p.kv_lens[b];
     s_off[b] = o;
@@ -47,6 +50,7 @@ __device__ __forceinline__ bool load_chunk(const ChunkParams& p, int* s_off, int
     if (len > (long long)p.max_pages * kPage) bad |= 2;
   }
   const bool b1 = __syncthreads_or(bad & 1), b2 = __syncthreads_or(bad & 2);
+  dead = __syncthreads_or(status != 0);
   if ((b1 || b2) && threadIdx.x == 0) set_status(p.status, b1 ? SDV_ERR_BAD_INPUT : SDV_ERR_PAGE_RANGE);
   return !b1 && !b2;
 }

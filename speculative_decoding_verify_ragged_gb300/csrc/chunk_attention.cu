@@ -116,8 +116,8 @@ __global__ void __launch_bounds__(CA_THREADS, per_sm<D, FMT, NT>()) chunk_attn_k
   const int group = p.c.n_q / p.c.n_kv, window = p.c.window;
   // a call that has failed already writes nothing, but still takes its part in
   // the counting below, so that the counters end at zero whichever block saw it
-  const bool dead = read_status(p.c.status) != 0;
-  if (!load_chunk(p.c, s_off, s_len)) return;
+  bool dead;
+  if (!load_chunk(p.c, s_off, s_len, dead)) return;
 
   // pages of each of a sequence's items (those that any of its rows sees), first page
   auto seq_of = [&](int b) {
