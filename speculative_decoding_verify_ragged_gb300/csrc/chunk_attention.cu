@@ -24,6 +24,7 @@ namespace {
 constexpr int CA_WARPS = 4;
 constexpr int CA_THREADS = CA_WARPS * kWarp;
 constexpr float kNoMax = -1e30f;  // the maximum before the first visible key
+constexpr int kFewItems = 4;      // blocks per item from which the items are cut by themselves
 constexpr int kMinPages = 4;      // pages a block takes at least: one per warp
 constexpr int kSplitBias = 8;     // e4m3: weights carry 2^(e + 8), in fp16's normal range for every e
 
@@ -107,7 +108,7 @@ __global__ void __launch_bounds__(CA_THREADS, per_sm<D, FMT, NT>()) chunk_attn_k
   long long* s_base = reinterpret_cast<long long*>(s_ml + CA_WARPS * 2 * ROWS);  // [B + 1] first unit of each sequence
   int* s_off = reinterpret_cast<int*>(s_base + p.c.B + 1);
   int* s_len = s_off + p.c.B + 1;
-  __shared__ long long s_scan[CA_WARPS];
+  __shared__ long long s_scan[CA_WARPS], s_items[CA_WARPS];
   __shared__ int s_last;
 
   griddep_launch_dependents();
@@ -130,15 +131,44 @@ __global__ void __launch_bounds__(CA_THREADS, per_sm<D, FMT, NT>()) chunk_attn_k
     return s.n > 0 ? max(1, (s.len + kPage - 1) / kPage - lo) : 0;
   };
   auto seq_tiles = [&](const SeqRows& s) { return (int)(((long long)s.n * group + ROWS - 1) / ROWS); };
+  // Units: pages, cut into equal runs over the blocks; a block that holds the end of
+  // one item and the beginning of another pays both items' latencies in turn.
+  // With few items they are cut by themselves instead, into pieces of `per_cta`
+  // pages, one a block (the sum over items of ceil(pages / per) is at most the
+  // blocks then), and a unit is a piece: 1 sequence of 517 tokens ALIGN_FIGURE.
+  const int per_thread = (B + CA_THREADS - 1) / CA_THREADS, b_lo = min(B, tid * per_thread), b_hi = min(B, b_lo + per_thread);
+  long long pages = 0, items = 0;
+  for (int b = b_lo; b < b_hi; ++b) {
+    const SeqRows s = seq_of(b);
+    int lo;
+    const long long n = (long long)seq_tiles(s) * p.c.n_kv;
+    pages += seq_pages(s, lo) * n;
+    items += n;
+  }
+  pages = warp_sum_u64(pages);
+  items = warp_sum_u64(items);
+  if (lane == 0) {
+    s_scan[warp] = pages;
+    s_items[warp] = items;
+  }
+  __syncthreads();
+  pages = items = 0;
+#pragma unroll
+  for (int w = 0; w < CA_WARPS; ++w) {
+    pages += s_scan[w];
+    items += s_items[w];
+  }
+  const bool pieces = items * kFewItems <= gridDim.x;
+  const long long blocks = pieces ? gridDim.x - items : gridDim.x;
+  const long long per_cta = max((long long)kMinPages, (pages + blocks - 1) / blocks);
   {
-    const int per = (B + CA_THREADS - 1) / CA_THREADS, b0 = min(B, tid * per), b1 = min(B, b0 + per);
     long long sum = 0;
-    for (int b = b0; b < b1; ++b) {
+    for (int b = b_lo; b < b_hi; ++b) {
       const SeqRows s = seq_of(b);
       int lo;
       const int u = seq_pages(s, lo);
       s_base[b] = sum;
-      sum += (long long)u * seq_tiles(s) * p.c.n_kv;
+      sum += (pieces ? (u + per_cta - 1) / per_cta : u) * seq_tiles(s) * p.c.n_kv;
     }
     long long inc = sum;
 #pragma unroll
@@ -146,19 +176,20 @@ __global__ void __launch_bounds__(CA_THREADS, per_sm<D, FMT, NT>()) chunk_attn_k
       const long long v = __shfl_up_sync(0xffffffffu, inc, o);
       if (lane >= o) inc += v;
     }
+    __syncthreads();  // the totals have been read
     if (lane == 31) s_scan[warp] = inc;
     __syncthreads();
     long long add = inc - sum;
     for (int w = 0; w < warp; ++w) add += s_scan[w];
-    for (int b = b0; b < b1; ++b) s_base[b] += add;
+    for (int b = b_lo; b < b_hi; ++b) s_base[b] += add;
     if (tid == CA_THREADS - 1) s_base[B] = add + sum;
     __syncthreads();
   }
   const long long units = s_base[B];
-  const long long per_cta = max((long long)kMinPages, (units + gridDim.x - 1) / gridDim.x);
-  const long long u_end = min(units, (blockIdx.x + 1) * per_cta);
+  const long long run = pieces ? 1 : per_cta;  // units of a block
+  const long long u_end = min(units, (blockIdx.x + 1) * run);
 
-  for (long long u = blockIdx.x * per_cta; u < u_end;) {
+  for (long long u = blockIdx.x * run; u < u_end;) {
     int b = 0;
     {
       int lo = 0, hi = B - 1;  // the last b with s_base[b] <= u (empty sequences share their successor's base)
@@ -172,15 +203,38 @@ __global__ void __launch_bounds__(CA_THREADS, per_sm<D, FMT, NT>()) chunk_attn_k
     const SeqRows sq = seq_of(b);
     int lo_page;
     const int n_pages = seq_pages(sq, lo_page), tiles = seq_tiles(sq);
-    const long long item = (u - s_base[b]) / n_pages;  // within the sequence: key head, then tile
-    const int page0 = static_cast<int>((u - s_base[b]) - item * n_pages);
-    const int h = static_cast<int>(item / tiles), row0 = static_cast<int>(item - (long long)h * tiles) * ROWS;
-    const int n_here = static_cast<int>(min(u_end - u, (long long)(n_pages - page0)));
+    // within the sequence: key head, then tile, then page (in 32 bits where they fit, as nearly always)
+    const long long in_seq = u - s_base[b];
+    const int item_units = pieces ? static_cast<int>((n_pages + per_cta - 1) / per_cta) : n_pages;
+    const long long item = units < 0x7FFFFFFF ? static_cast<unsigned>(in_seq) / static_cast<unsigned>(item_units) : in_seq / item_units;
+    const int at_unit = static_cast<int>(in_seq - item * item_units), page0 = pieces ? static_cast<int>(at_unit * per_cta) : at_unit;
+    const int h = units < 0x7FFFFFFF ? static_cast<unsigned>(item) / static_cast<unsigned>(tiles) : static_cast<int>(item / tiles);
+    const int row0 = static_cast<int>(item - (long long)h * tiles) * ROWS;
+    const int n_here = static_cast<int>(min(pieces ? per_cta : u_end - u, (long long)(n_pages - page0)));
     const int n_rows = static_cast<int>(min((long long)ROWS, (long long)sq.n * group - row0));
     const int pmin = sq.pos0 + row0 / group, pmax = sq.pos0 + (row0 + n_rows - 1) / group;
     // pages of this run that a row of the item sees
     const int first = max(lo_page + page0, window > 0 ? max(0, pmin - window + 1) / kPage : 0);
     const int last = min(lo_page + page0 + n_here, pmax < 0 ? 0 : pmax / kPage + 1);
+
+    const int pg0 = first + warp;
+    const int mine = dead || pg0 >= last ? 0 : (last - pg0 + CA_WARPS - 1) / CA_WARPS;  // this warp's pages
+    int ids = 0;
+    Frag<D, FMT> nxt, cur;
+    auto page_id = [&](int i) {  // the warp's i-th page; the lanes fetch 32 ids at a time
+      if ((i & 31) == 0) {
+        ids = -1;
+        if (i + lane < mine) {
+          ids = p.c.page_table[(long long)b * p.c.max_pages + pg0 + (i + lane) * CA_WARPS];
+          if (ids < 0 || ids >= p.c.pool_pages) {
+            set_status(p.c.status, SDV_ERR_PAGE_RANGE);
+            ids = 0;  // some page of the pool: the call's outputs hold nothing meaningful
+          }
+        }
+      }
+      return __shfl_sync(0xffffffffu, ids, i & 31);
+    };
+    if (mine > 0) load_page(nxt, p.c, page_id(0), h, g, t);
 
     // queries: row g of each 8, laid out like the keys; the rows whose scores
     // this lane holds are 2 t and 2 t + 1 of each 8
@@ -243,24 +297,6 @@ __global__ void __launch_bounds__(CA_THREADS, per_sm<D, FMT, NT>()) chunk_attn_k
       l[r][0] = l[r][1] = 0.f;
     }
 
-    const int pg0 = first + warp;
-    const int mine = dead || pg0 >= last ? 0 : (last - pg0 + CA_WARPS - 1) / CA_WARPS;  // this warp's pages
-    int ids = 0;
-    Frag<D, FMT> nxt, cur;
-    auto page_id = [&](int i) {  // the warp's i-th page; the lanes fetch 32 ids at a time
-      if ((i & 31) == 0) {
-        ids = -1;
-        if (i + lane < mine) {
-          ids = p.c.page_table[(long long)b * p.c.max_pages + pg0 + (i + lane) * CA_WARPS];
-          if (ids < 0 || ids >= p.c.pool_pages) {
-            set_status(p.c.status, SDV_ERR_PAGE_RANGE);
-            ids = 0;  // some page of the pool: the call's outputs hold nothing meaningful
-          }
-        }
-      }
-      return __shfl_sync(0xffffffffu, ids, i & 31);
-    };
-    if (mine > 0) load_page(nxt, p.c, page_id(0), h, g, t);
     for (int i = 0; i < mine; ++i) {
       cur = nxt;
       if (i + 1 < mine) load_page(nxt, p.c, page_id(i + 1), h, g, t);
@@ -411,8 +447,10 @@ __global__ void __launch_bounds__(CA_THREADS, per_sm<D, FMT, NT>()) chunk_attn_k
       for (int j = 0; j < PER; ++j) acc[j] += a * s_o[(w * ROWS + row) * D + c0 + j];
     }
     // the blocks that hold pages of this item
-    const long long u0 = s_base[b] + item * n_pages;
-    const int c_first = static_cast<int>(u0 / per_cta), c_last = static_cast<int>((u0 + n_pages - 1) / per_cta);
+    const long long u0 = s_base[b] + item * item_units;
+    const bool small = units < 0x7FFFFFFF;
+    const int c_first = small ? static_cast<unsigned>(u0) / static_cast<unsigned>(run) : static_cast<int>(u0 / run);
+    const int c_last = small ? static_cast<unsigned>(u0 + item_units - 1) / static_cast<unsigned>(run) : static_cast<int>((u0 + item_units - 1) / run);
     bool write = row < n_rows && !dead;
     if (c_first != c_last) {
       // a block has at most two cut items: one begun before its run (slot 0)
@@ -437,11 +475,13 @@ __global__ void __launch_bounds__(CA_THREADS, per_sm<D, FMT, NT>()) chunk_attn_k
       write = write && s_last;
       if (s_last) {
         M = kNoMax;
+#pragma unroll 8
         for (int cta = c_first; cta <= c_last; ++cta)
           M = fmaxf(M, __ldcg(p.part + (2LL * cta + (cta == c_first)) * PF + kItemRows * D + row));
         L = 0.f;
 #pragma unroll
         for (int j = 0; j < PER; ++j) acc[j] = 0.f;
+#pragma unroll 4
         for (int cta = c_first; cta <= c_last; ++cta) {
           const float* src = p.part + (2LL * cta + (cta == c_first)) * PF;
           const float a = fast_ex2(__ldcg(src + kItemRows * D + row) - M);
@@ -464,7 +504,7 @@ __global__ void __launch_bounds__(CA_THREADS, per_sm<D, FMT, NT>()) chunk_attn_k
             make_uint2(pack_bf16x2(acc[j] * inv, acc[j + 1] * inv), pack_bf16x2(acc[j + 2] * inv, acc[j + 3] * inv));
     }
     __syncthreads();
-    u += n_here;
+    u += pieces ? 1 : n_here;
   }
 }
 
