@@ -92,10 +92,19 @@ __device__ __forceinline__ void load_page(Frag<D, FMT>& f, const ChunkParams& c,
   }
 }
 
+// What the end of an item needs: out of the registers of the pages' loop.
+struct ItemEnd {
+  int off, head, row0, rows, first, last, units;
+};
+struct Plan {
+  long long per, run;  // pages of a piece; units of a block
+  bool pieces;
+};
+
 // Blocks per SM: what the registers allow (held: two pages, the output, the queries).
 template <int D, int FMT, int NT>
 constexpr int per_sm() {
-  return D == 64 ? 4 : FMT == SDV_CACHE_E4M3 ? (NT == 1 ? 3 : 2) : 2;
+  return D == 64 ? (NT == 1 ? 4 : 3) : FMT == SDV_CACHE_E4M3 ? (NT == 1 ? 3 : 2) : 2;
 }
 
 template <int D, int FMT, int NT>
@@ -109,6 +118,8 @@ __global__ void __launch_bounds__(CA_THREADS, per_sm<D, FMT, NT>()) chunk_attn_k
   int* s_off = reinterpret_cast<int*>(s_base + p.c.B + 1);
   int* s_len = s_off + p.c.B + 1;
   __shared__ long long s_scan[CA_WARPS], s_items[CA_WARPS];
+  __shared__ Plan s_plan;
+  __shared__ ItemEnd s_end;
   __shared__ int s_last;
 
   griddep_launch_dependents();
@@ -183,13 +194,15 @@ __global__ void __launch_bounds__(CA_THREADS, per_sm<D, FMT, NT>()) chunk_attn_k
     for (int w = 0; w < warp; ++w) add += s_scan[w];
     for (int b = b_lo; b < b_hi; ++b) s_base[b] += add;
     if (tid == CA_THREADS - 1) s_base[B] = add + sum;
+    if (tid == 0) s_plan = Plan{per_cta, pieces ? 1 : per_cta, pieces};
     __syncthreads();
   }
-  const long long units = s_base[B];
-  const long long run = pieces ? 1 : per_cta;  // units of a block
-  const long long u_end = min(units, (blockIdx.x + 1) * run);
 
-  for (long long u = blockIdx.x * run; u < u_end;) {
+  for (long long u = blockIdx.x * s_plan.run;;) {
+    // (the plan is read anew for each item: held across the pages it would spill)
+    const bool pieces = s_plan.pieces;
+    const long long units = s_base[B], per_cta = s_plan.per, run = s_plan.run, u_end = min(units, (blockIdx.x + 1) * run);
+    if (u >= u_end) break;
     int b = 0;
     {
       int lo = 0, hi = B - 1;  // the last b with s_base[b] <= u (empty sequences share their successor's base)
@@ -212,6 +225,15 @@ __global__ void __launch_bounds__(CA_THREADS, per_sm<D, FMT, NT>()) chunk_attn_k
     const int row0 = static_cast<int>(item - (long long)h * tiles) * ROWS;
     const int n_here = static_cast<int>(min(pieces ? per_cta : u_end - u, (long long)(n_pages - page0)));
     const int n_rows = static_cast<int>(min((long long)ROWS, (long long)sq.n * group - row0));
+    if (tid == 0) {
+      // with the blocks that hold pages of this item
+      const long long u0 = s_base[b] + item * item_units, u1 = u0 + item_units - 1;
+      const bool small = units < 0x7FFFFFFF;
+      s_end = ItemEnd{sq.off, h * group, row0, n_rows,
+                      small ? static_cast<int>(static_cast<unsigned>(u0) / static_cast<unsigned>(run)) : static_cast<int>(u0 / run),
+                      small ? static_cast<int>(static_cast<unsigned>(u1) / static_cast<unsigned>(run)) : static_cast<int>(u1 / run),
+                      pieces ? 1 : n_here};
+    }
     const int pmin = sq.pos0 + row0 / group, pmax = sq.pos0 + (row0 + n_rows - 1) / group;
     // pages of this run that a row of the item sees
     const int first = max(lo_page + page0, window > 0 ? max(0, pmin - window + 1) / kPage : 0);
@@ -446,12 +468,9 @@ __global__ void __launch_bounds__(CA_THREADS, per_sm<D, FMT, NT>()) chunk_attn_k
 #pragma unroll
       for (int j = 0; j < PER; ++j) acc[j] += a * s_o[(w * ROWS + row) * D + c0 + j];
     }
-    // the blocks that hold pages of this item
-    const long long u0 = s_base[b] + item * item_units;
-    const bool small = units < 0x7FFFFFFF;
-    const int c_first = small ? static_cast<unsigned>(u0) / static_cast<unsigned>(run) : static_cast<int>(u0 / run);
-    const int c_last = small ? static_cast<unsigned>(u0 + item_units - 1) / static_cast<unsigned>(run) : static_cast<int>((u0 + item_units - 1) / run);
-    bool write = row < n_rows && !dead;
+    const ItemEnd e = s_end;
+    const int c_first = e.first, c_last = e.last;
+    bool write = row < e.rows && !dead;
     if (c_first != c_last) {
       // a block has at most two cut items: one begun before its run (slot 0)
       // and one that goes on behind it (slot 1)
@@ -496,15 +515,15 @@ __global__ void __launch_bounds__(CA_THREADS, per_sm<D, FMT, NT>()) chunk_attn_k
     }
     if (write) {
       const float inv = L == 0.f ? 0.f : 1.f / L;  // a row that sees nothing gives 0
-      const int rr = row0 + row;
-      __nv_bfloat16* dst = p.out + (long long)(sq.off + rr / group) * p.out_stride + (long long)(h * group + rr % group) * D + c0;
+      const int rr = e.row0 + row;
+      __nv_bfloat16* dst = p.out + (long long)(e.off + rr / group) * p.out_stride + (long long)(e.head + rr % group) * D + c0;
 #pragma unroll
       for (int j = 0; j < PER; j += 4)
         *reinterpret_cast<uint2*>(dst + j) =
             make_uint2(pack_bf16x2(acc[j] * inv, acc[j + 1] * inv), pack_bf16x2(acc[j + 2] * inv, acc[j + 3] * inv));
     }
     __syncthreads();
-    u += pieces ? 1 : n_here;
+    u += e.units;
   }
 }
 
