@@ -80,8 +80,8 @@ typedef struct sdv_cache sdv_cache;
 size_t sdv_cache_workspace_size(const sdv_cache_config *cfg, int max_rows, int max_slots);
 
 /* Create a handle on the current device.  `workspace` (device, caller-owned, >=
- * sdv_cache_workspace_size bytes, 256-byte aligned) is cleared here on `stream` and used by
- * every sdv_cache_attention of this handle, so those calls must not overlap in
+ * sdv_cache_workspace_size bytes, 256-byte aligned) has its counters cleared here, on `stream`, which
+ * is synchronised (so not inside a capture); it is used by every sdv_cache_attention of this handle, so those calls must not overlap in
  * time; graphs captured on one handle must not run at the same time either.
  * Calls are made with the handle's device current. */
 sdv_status sdv_cache_create(const sdv_cache_config *cfg, void *workspace, size_t workspace_bytes, int max_rows,

@@ -138,7 +138,9 @@ extern "C" sdv_status sdv_cache_create(const sdv_cache_config* cfg, void* worksp
       h->turns.f[j] = static_cast<unsigned long long>(std::ldexp(turn, 64));
     }
   }
+  // cleared before the call returns, so that the first calls may come on any stream
   e = cudaMemsetAsync(h->counters, 0, s.part, static_cast<cudaStream_t>(stream));
+  if (e == cudaSuccess) e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) {
     delete h;
     return cuda_fail(e);

@@ -439,3 +439,92 @@ def test_a_prompt_in_pieces_then_drafts(fmt):
         eng.attention(t["q"].float().contiguous(), batch, out32, st)
         assert st.item() == 0
         _close(out32.view(4, n_q, d), want, tol)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_next_tokens_beside_pieces_of_prompts(fmt, d):
+    """A step that mixes single tokens with long pieces (both kernels take a share), one without the
+    hint of it (one kernel takes all), and a batch of pieces whose last tiles are nearly empty."""
+    for q, kv in (([1] * 10 + [200, 40, 0, 3], [700, 16, 33, 5, 900, 1, 250, 64, 129, 400, 1000, 41, 9, 800]),
+                  ([1, 300, 2], [500, 650, 2]), ([65, 129, 33, 257], [65, 1000, 70, 257])):
+        s = ch.make(q, kv, 8, 2, d, fmt, seed=sum(q))
+        want, tol = ch.attention(s)
+        _close(_attend(s), want, tol)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+def test_one_handle_over_many_shapes(fmt):
+    """Calls of unlike shapes one after another on one handle, nothing waited for between them: what one leaves
+    in the workspace (parts, counters) is never seen by the next."""
+    shapes = [([1], [3000]), ([300, 2], [900, 40]), ([1] * 40, list(range(1, 4001, 100))), ([64], [9000]), ([1000], [1000]),
+              ([3, 1], [20, 7000]), ([128, 16], [128, 2000])]
+    cases = [ch.make(q, kv, 16, 4, 128, fmt, seed=i) for i, (q, kv) in enumerate(shapes)]
+    c = _cache(cases[0], rows=1200, slots=64)
+    chunks = [_chunk(c, s) for s in cases]
+    first = []
+    for s, k in zip(cases, chunks):
+        out = torch.empty_like(s["q"])
+        c.attention(k, s["q"], out, s["status"])
+        torch.cuda.synchronize()
+        want, tol = ch.attention(s)
+        _close(out, want, tol)
+        first.append(out)
+    g = torch.Generator().manual_seed(1)
+    order = [int(i) for _ in range(20) for i in torch.randperm(len(cases), generator=g)]
+    outs = [torch.empty_like(cases[i]["q"]) for i in order]
+    for i, out in zip(order, outs):
+        c.attention(chunks[i], cases[i]["q"], out, cases[i]["status"])
+    torch.cuda.synchronize()
+    for i, out in zip(order, outs):
+        assert cases[i]["status"].item() == 0 and torch.equal(out, first[i])
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("q_lens,kv_lens", [([4, 1], [300, 90]), ([150, 9], [700, 90])])
+def test_rows_that_are_not_numbers_stay_alone(fmt, q_lens, kv_lens):
+    """NaN and infinite queries give NaN in their own rows and heads and nothing elsewhere; keys that are
+    NaN where no earlier row sees them change no earlier row."""
+    s = ch.make(q_lens, kv_lens, 8, 2, 128, fmt, seed=4)
+    want, tol = ch.attention(s)
+    q = s["q"].clone()
+    s["q"][1, 3] = float("nan")
+    s["q"][2, 5, 7] = float("inf")
+    out = torch.empty_like(q)
+    c = _cache(s)
+    c.attention(_chunk(c, s), s["q"], out, s["status"])
+    assert s["status"].item() == 0
+    odd = torch.zeros(q.shape[:2], dtype=torch.bool, device="cuda")
+    odd[1, 3] = odd[2, 5] = True
+    assert torch.isnan(out[odd]).all()
+    _close(out[~odd], want[~odd], tol[~odd])
+    # the newest key of sequence 0 is a NaN: the rows before the newest are as they were
+    s["q"].copy_(q)
+    at = kv_lens[0] - 1
+    page = int(s["table"][0, at // 16])
+    if fmt == "bf16":
+        s["pool"][page, :, 0, at % 16] = float("nan")
+    else:
+        s["pool"][page, :, 0, at % 16] = 0x7F
+    c.attention(_chunk(c, s), s["q"], out, s["status"])
+    keep = torch.ones(s["T"], dtype=torch.bool, device="cuda")
+    keep[q_lens[0] - 1] = False
+    assert torch.isnan(out[q_lens[0] - 1]).all()
+    _close(out[keep], want[keep], tol[keep])
+
+
+@pytest.mark.parametrize("q,kv", [(1, 600), (200, 700)])
+@pytest.mark.parametrize("e", [-15, 7])
+def test_attention_at_the_scales_ends(q, kv, e):
+    """Keys and values under the smallest and the largest scale."""
+    s = ch.make([q], [kv], 8, 2, 128, "e4m3", seed=8, tail=0.0)
+    used = s["scales"] <= 134
+    byte = torch.full_like(s["scales"], e + 127)
+    shift = torch.exp2(e - (s["scales"].double() - 127))
+    s["values"] = s["values"] * torch.where(used, shift, torch.ones_like(shift))[..., None]
+    s["scales"] = torch.where(used, byte, s["scales"])
+    s["q"] = (s["q"].float() * 2.0 ** (-6 - e)).to(torch.bfloat16)
+    want, tol = ch.attention(s)
+    out = _attend(s)
+    # (tol's term for small weights is of a value of 448 at scale 2^0)
+    _close(out, want, tol * max(1.0, 2.0 ** e))
