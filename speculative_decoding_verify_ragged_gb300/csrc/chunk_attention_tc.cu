@@ -1,24 +1,40 @@
 // Attention of a ragged chunk over the paged cache on the 5th-generation tensor
-// cores, for sequences whose rows fill a 128-row tile (prompts, pieces of them).
+// cores, for sequences of more than 16 packed rows (prompts, pieces of them, many drafts).
 //
 // An item is two tiles of 128 packed query rows (row = token, head of the group)
 // of one (sequence, key head) against the blocks of 128 keys that they see.  The
-// items' blocks are laid end to end and cut into equal runs, one per SM; the
-// parts of an item cut between SMs are joined in the runs' order.  Per block
-//   S_t = Q_t K^T  (M = 128 rows, N = 128 keys),  O_t += P_t V  (P_t from TMEM)
-// run for tile 0 and tile 1 in turn, so the tensor cores work on one tile while
-// the other's softmax runs: one thread holds one row, reads its scores from
-// TMEM once and writes the weights over them in 16 bits.  The running maximum is a
-// bound, set by the first block and moved only when a block's weights add up
-// to more than kMost (then the block is taken again and O is rescaled in TMEM): their sum,
-// which is needed anyway, stands in for a maximum.
+// items' blocks are laid end to end, weighed by what they cost, and cut into
+// equal runs, one per SM; the parts of an item cut between SMs are joined in the
+// runs' order, so equal inputs give equal bits.  Per step of 64 keys and tile t
+//   S_t = Q_t K^T  (M = 128 rows, N = 64 keys),  O_t += P_t V  (P_t from TMEM):
+// one thread issues each tile's products, S of the next step before this step's
+// softmax is waited for, into the other of two buffers; a thread of the softmax
+// holds one row, reads its scores from TMEM once and writes the weights over
+// them in 16 bits (bf16 with a bf16 cache, fp16 with codes: half a step of each
+// weight is the one rounding between the scores and the output's own).
+// The running maximum is a bound, set by the first step and moved only when a
+// step's weights add up to more than kMost (then the step is taken again and O is
+// rescaled in TMEM): their sum, which is needed anyway, stands in for a maximum.
 //
-// TMEM: S_0, S_1 (128 columns each; P_t over S_t's first 64), O_0, O_1 (D each).
+// TMEM: two buffers of S_t for each tile (64 columns, P over the first 32), O_0, O_1.
 // Shared memory: Q tiles and a ring of K and V blocks, rows of 128 bytes,
-// 128-byte swizzle.  A bf16 cache is loaded by TMA, a page's 64-wide half a copy; e4m3
-// codes go through registers (four warps) and land as fp16, scales applied, exact.
-// Values of keys that a block's rows cannot see are zeroed in shared memory, so
-// that nothing behind a sequence's end is ever multiplied.
+// 128-byte swizzle.  A bf16 cache is loaded by TMA, a page's 64-wide half a copy,
+// by two warps; e4m3 codes go through four warps' registers and land as fp16, scales
+// applied, exact.  Values of keys that an item's rows cannot see are zeroed in
+// shared memory, so that nothing behind a sequence's end is ever multiplied.
+//
+// What bounds it, 32 query and 8 key heads of 128, bf16: 2048 new tokens over 32749
+// take 665 us in a graph's replays (1600 TFLOP/s, 0.84 of the burst peak, 0.94 of the sustained one; back
+// to back for long the power limit holds it at 740 us).  A block of two tiles takes 3060 cycles: its
+// products 2560 (N = 64 scores wait for shared memory: 48 cycles each in place
+// of 32, measured), the rest is the round from a step's weights to the scores
+// after next.  Scores of 128 keys at once into one buffer, their weights in
+// halves, the tiles taking turns, were slower (903 us: the softmax waits for each round).  One
+// issuing thread for both tiles under `lane == 0` issued at 70 cycles a product (1001 us).
+// With codes the same work takes 890 us: the conversion's instructions
+// and loads lengthen the softmax from 870 to 1400 cycles a step; neither deeper loads,
+// fewer instructions in the conversion nor other register shares changed that.
+//
 #include "chunk.cuh"
 #include "tcgen05.cuh"
 
