@@ -64,7 +64,7 @@ sdv_status chunk_params(const sdv_cache* h, const sdv_chunk* c, int* status, Chu
   if (!h || !c || !status) return SDV_ERR_INVALID_ARG;
   if (c->B <= 0 || c->T < 0 || c->max_q < 0 || c->window < 0 || c->num_pool_pages <= 0 || c->max_pages_per_seq <= 0)
     return SDV_ERR_INVALID_ARG;
-  if (c->max_pages_per_seq > (1 << 26)) return SDV_ERR_INVALID_ARG;  // positions fit 31 bits
+  if (c->max_pages_per_seq > (1 << 26)) return SDV_ERR_INVALID_ARG;  // positions below 2^30
   if (!c->row_offsets || !c->kv_lens || !c->kv_pool || !c->page_table || !aligned16(c->kv_pool)) return SDV_ERR_INVALID_ARG;
   if (h->cfg.cache_format == SDV_CACHE_E4M3 && (!c->kv_scales || !aligned16(c->kv_scales))) return SDV_ERR_INVALID_ARG;
   if (c->B > h->max_slots || c->T > h->max_rows) return SDV_ERR_CAPACITY;
@@ -73,7 +73,7 @@ sdv_status chunk_params(const sdv_cache* h, const sdv_chunk* c, int* status, Chu
   p->B = c->B;
   p->T = c->T;
   p->max_q = c->max_q;
-  p->window = c->window;
+  p->window = c->window < (1 << 30) ? c->window : 0;  // positions end before 2^30: a window as long sees all
   p->row_offsets = c->row_offsets;
   p->kv_lens = c->kv_lens;
   p->pool = static_cast<uint8_t*>(c->kv_pool);
@@ -215,6 +215,10 @@ extern "C" sdv_status sdv_cache_attention(sdv_cache* h, const sdv_chunk* chunk, 
     const cudaError_t e = launch_chunk_attn_tc(d, h->cfg.cache_format, map, p, h->sms, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e);
     if (!two) return SDV_OK;
+    // (mostly single tokens: items of 8 rows, two for a sequence of up to 16)
+    p.part = h->part;
+    p.counters = h->counters;
+    return launched(launch_chunk_attn(d, h->cfg.cache_format, group <= 8, p, h->sms, static_cast<cudaStream_t>(stream)));
   }
   p.part = h->part;
   p.counters = h->counters;

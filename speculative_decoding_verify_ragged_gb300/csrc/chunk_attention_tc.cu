@@ -270,7 +270,6 @@ __global__ void __launch_bounds__(Cfg<D, FMT>::THREADS, 1)
     chunk_attn_tc_kernel(const __grid_constant__ CUtensorMap tmKV, const ChunkAttnParams p) {
   using C = Cfg<D, FMT>;
   extern __shared__ uint8_t smem_raw[];
-  griddep_launch_dependents();
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
   uint64_t* empty = full + C::NS;
@@ -317,6 +316,7 @@ __global__ void __launch_bounds__(Cfg<D, FMT>::THREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+  griddep_launch_dependents();  // (only now that this block has its TMEM)
   griddep_wait();
 
   const int B = p.c.B, group = p.c.n_q / p.c.n_kv, window = p.c.window, n_kv = p.c.n_kv;
@@ -347,10 +347,10 @@ __global__ void __launch_bounds__(Cfg<D, FMT>::THREADS, 1)
   long long u_begin = 0, u_end = 0, per_cta = 1;
   if (good) {
     // units (blocks times tiles) of one key head of each sequence, a warp a sequence, into the ring (not in use yet)
-    int* s_units = reinterpret_cast<int*>(smem);                                                 // [B]
+    long long* s_units = reinterpret_cast<long long*>(smem);  // [B]
     for (int b = warp; b < B; b += blockDim.x / kWarp) {
       const SeqRows s = seq_of(b);
-      int sum = 0;
+      long long sum = 0;
       for (int qt = lane; qt < items_of(s); qt += kWarp) {
         sum += units_of(make_item(s, group, window, qt));
       }
@@ -363,7 +363,7 @@ __global__ void __launch_bounds__(Cfg<D, FMT>::THREADS, 1)
       // total, then the sequence, key head, item and block of the run's first unit
       long long total = 0;
       for (int b0 = 0; b0 < B; b0 += kWarp) {
-        long long v = b0 + lane < B ? (long long)s_units[b0 + lane] * n_kv : 0;
+        long long v = b0 + lane < B ? s_units[b0 + lane] * n_kv : 0;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
         total += v;
@@ -374,7 +374,7 @@ __global__ void __launch_bounds__(Cfg<D, FMT>::THREADS, 1)
         long long base = 0;
         int b = -1;
         for (int b0 = 0; b0 < B && b < 0; b0 += kWarp) {
-          const long long v = b0 + lane < B ? (long long)s_units[b0 + lane] * n_kv : 0;
+          const long long v = b0 + lane < B ? s_units[b0 + lane] * n_kv : 0;
           long long inc = v;
 #pragma unroll
           for (int o = 1; o < 32; o <<= 1) {
@@ -391,14 +391,16 @@ __global__ void __launch_bounds__(Cfg<D, FMT>::THREADS, 1)
           }
         }
         const SeqRows s = seq_of(b);
-        const int per_head = s_units[b], h = static_cast<int>((u - base) / per_head);
-        int rest = static_cast<int>((u - base) - (long long)h * per_head), qt = -1;
+        const long long per_head = s_units[b];
+        const int h = static_cast<int>((u - base) / per_head);
+        long long rest = (u - base) - h * per_head;
+        int qt = -1;
         for (int q0 = 0; qt < 0; q0 += kWarp) {
-          const int v = q0 + lane < items_of(s) ? units_of(make_item(s, group, window, q0 + lane)) : 0;
-          int inc = v;
+          const long long v = q0 + lane < items_of(s) ? units_of(make_item(s, group, window, q0 + lane)) : 0;
+          long long inc = v;
 #pragma unroll
           for (int o = 1; o < 32; o <<= 1) {
-            const int w = __shfl_up_sync(0xffffffffu, inc, o);
+            const long long w = __shfl_up_sync(0xffffffffu, inc, o);
             if (lane >= o) inc += w;
           }
           const unsigned hit = __ballot_sync(0xffffffffu, inc > rest);
@@ -413,7 +415,7 @@ __global__ void __launch_bounds__(Cfg<D, FMT>::THREADS, 1)
         if (lane == 0) {
           // the first block that begins at the run's first unit or behind it
           const int w = weight(make_item(s, group, window, qt));
-          s_start = Place{b, h, qt, (max(0, rest - kItemCost) + w - 1) / w, u - rest};
+          s_start = Place{b, h, qt, static_cast<int>((max(0LL, rest - kItemCost) + w - 1) / w), u - rest};
         }
       }
       if (lane == 0) {

@@ -56,7 +56,7 @@ def test_attention(fmt, heads, lens):
 
 
 @pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
-@pytest.mark.parametrize("window", [1, 7, 16, 100, 5000])
+@pytest.mark.parametrize("window", [1, 7, 16, 100, 5000, 2 ** 31 - 1])
 def test_attention_window(fmt, window):
     s = ch.make([1, 40, 257, 2], [300, 40, 600, 33], 8, 2, 128, fmt, seed=window, window=window)
     want, tol = ch.attention(s)
