@@ -140,6 +140,12 @@ __device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity) {
   return mbar_wait(bar, parity);
 }
 
+// 16 bytes into shared memory, or 16 zeros (bytes = 0: src is not read).
+__device__ __forceinline__ void cp_async16(void* dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 // Registers per thread of this warpgroup (the shares of all add up to the launch's).
 template <int N>
 __device__ __forceinline__ void regs_up() {
@@ -239,7 +245,7 @@ __device__ __forceinline__ Tile make_tile(const SeqRows& s, const Item& it, int 
 // of one tile takes 2450 cycles against 2750 and an item begins at 3.7 blocks.
 // (With every block alike the SMs with the short items ended last: 4096 new tokens 193 us.)
 __device__ __forceinline__ int weight(const Item& it) { return it.rows > BM ? 8 : 7; }
-constexpr int kItemCost = 28;
+constexpr int kItemCost = 36;
 __device__ __forceinline__ int units_of(const Item& it) { return kItemCost + it.blocks * weight(it); }
 
 // A part of a run: blocks [b0, b1) of an item of (sequence b, key head h) whose first unit is u0.
@@ -432,7 +438,7 @@ __global__ void __launch_bounds__(Cfg<D, FMT>::THREADS, 1)
   // the parts of the run, one after another; a block is of the run that its first unit falls in
   auto end_block = [&](const Part& x) {  // blocks of x that begin before the run's end
     const int w = weight(x.it);
-    return static_cast<int>(min((long long)x.it.blocks, max(0LL, u_end - x.u0 - kItemCost + w - 1) / w));
+    return (static_cast<int>(min((long long)x.it.blocks * w, max(0LL, u_end - x.u0 - kItemCost))) + w - 1) / w;
   };
   auto next_part = [&](Part& x) {
     {
@@ -776,39 +782,46 @@ __global__ void __launch_bounds__(Cfg<D, FMT>::THREADS, 1)
       float cz = p.scale_log2;
       if (x.s0 < x.s1 && !dead) {
         // this row's query into the tile (its last readers are done: the scores were all seen)
-        // the warp's 32 rows, D / 8 lanes a row
+        // the warp's 32 rows, D / 8 lanes a row.  (Short loops here and in the
+        // output: this code runs once an item, and unrolled it was fetched
+        // anew each time, 9000 cycles where the copies take 2000.)
         constexpr int QL = D / 8, QR = kWarp / QL;  // lanes a row, rows a pass
         const long long mine = in_next ? (long long)(s.off + row / group) * p.q_stride + (long long)(part.h * group + row % group) * D : -1;
         const int ch = lane % QL, sub = lane / QL;
-        uint8_t* q_rows = smem + C::OFF_Q + t * C::SLOT + (ch >> 3) * HALF + (i & ~31) * 128;
-        uint4 w[QL];
-#pragma unroll
+        uint8_t* q_tile = smem + C::OFF_Q + t * C::SLOT;
+#pragma unroll 2
         for (int k = 0; k < QL; ++k) {
           const long long at = __shfl_sync(0xffffffffu, mine, k * QR + sub);
-          w[k] = at >= 0 ? *reinterpret_cast<const uint4*>(p.q + at + ch * 8) : make_uint4(0u, 0u, 0u, 0u);
+          const int r = (i & ~31) + k * QR + sub;
+          cp_async16(q_tile + (ch >> 3) * HALF + r * 128 + (((ch & 7) ^ (r & 7)) << 4), p.q + (at >= 0 ? at + ch * 8 : 0), at >= 0 ? 16 : 0);
         }
-#pragma unroll
-        for (int k = 0; k < QL; ++k) {
-          if constexpr (C::kCodes) {
-            // fp16 with the row's largest magnitude in [1/2, 1)
-            uint32_t* v = &w[k].x;
-            float a = 0.f;
-#pragma unroll
-            for (int x = 0; x < 4; ++x) a = fmaxf(a, fmaxf(fabsf(__uint_as_float(v[x] << 16)), fabsf(__uint_as_float(v[x] & 0xFFFF0000u))));
-#pragma unroll
-            for (int d = 1; d < QL; d <<= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, d));
-            const int e = min(max(static_cast<int>(__float_as_uint(a) >> 23) - 126, -100), 100);
-            const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+        cp_async_wait_all();
+        __syncwarp();
+        if constexpr (C::kCodes) {
+          // each thread its own row: fp16 with the largest magnitude in [1/2, 1)
+          __nv_bfloat162 top = __float2bfloat162_rn(0.f);
+#pragma unroll 4
+          for (int c = 0; c < QL; ++c) {
+            const uint4 w = *reinterpret_cast<const uint4*>(q_tile + (c >> 3) * HALF + i * 128 + (((c & 7) ^ (i & 7)) << 4));
+            const __nv_bfloat162* v = reinterpret_cast<const __nv_bfloat162*>(&w);
+            top = __hmax2(top, __hmax2(__hmax2(__habs2(v[0]), __habs2(v[1])), __hmax2(__habs2(v[2]), __habs2(v[3]))));
+          }
+          const float a = fmaxf(__low2float(top), __high2float(top));
+          const int e = min(max(static_cast<int>(__float_as_uint(a) >> 23) - 126, -100), 100);
+          const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+          cz = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+#pragma unroll 2
+          for (int c = 0; c < QL; ++c) {
+            uint4* at = reinterpret_cast<uint4*>(q_tile + (c >> 3) * HALF + i * 128 + (((c & 7) ^ (i & 7)) << 4));
+            uint4 w = *at;
+            uint32_t* v = &w.x;
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
               const __half2 y = __floats2half2_rn(__uint_as_float(v[x] << 16) * inv, __uint_as_float(v[x] & 0xFFFF0000u) * inv);
               v[x] = *reinterpret_cast<const uint32_t*>(&y);
             }
-            const int er = __shfl_sync(0xffffffffu, e, (lane % QR) * QL);  // the exponent of row k QR + lane % QR
-            if (lane / QR == k) cz = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + er) << 23);
+            *at = w;
           }
-          const int r = k * QR + sub;
-          *reinterpret_cast<uint4*>(q_rows + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = w[k];
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -845,7 +858,7 @@ __global__ void __launch_bounds__(Cfg<D, FMT>::THREADS, 1)
           if (!last) {
             float* mine = part_slot(p.part, D, blockIdx.x, c_first, t);
             if (went && !dead) {
-#pragma unroll
+#pragma unroll 1
               for (int c = 0; c < D / 32; ++c) {
                 uint32_t r[32];
                 tmem_ld32(t_o + 32 * c, r);
@@ -898,7 +911,7 @@ __global__ void __launch_bounds__(Cfg<D, FMT>::THREADS, 1)
         const float inv = l == 0.f ? 0.f : 1.f / l;  // a row that sees nothing gives 0
         const long long out_at = write ? (long long)(e.off + e_row / group) * p.out_stride + (long long)(e.h * group + e_row % group) * D : -1;
         if (others == 0 || __any_sync(0xffffffffu, join && write)) {
-#pragma unroll
+#pragma unroll(C::kCodes ? 1 : D / 32)
           for (int c = 0; c < D / 32; ++c) {
             uint32_t r[32];
             if (went && !dead) {
@@ -961,8 +974,9 @@ __global__ void __launch_bounds__(Cfg<D, FMT>::THREADS, 1)
       }
       if (!more) break;
       {
-        const int c_first = static_cast<int>((part.u0 + kItemCost) / per_cta);
-        const int c_last = static_cast<int>((part.u0 + kItemCost + (long long)(it.blocks - 1) * weight(it)) / per_cta);
+        const long long ua = part.u0 + kItemCost, ub = ua + (long long)(it.blocks - 1) * weight(it);  // the first and last block's units
+        const int c_first = ua >= u_begin ? (int)blockIdx.x : static_cast<int>(ua / per_cta);
+        const int c_last = ub < u_end ? (int)blockIdx.x : static_cast<int>(ub / per_cta);
         __syncwarp();
         if (lane == 0) s_held[warp] = Held{s.off, part.h, it.row0, it.rows, c_first, c_last, x.s0 < x.s1};
         if (tid == 0 && c_last - c_first > kJoinHere && c_first == (int)blockIdx.x) {
