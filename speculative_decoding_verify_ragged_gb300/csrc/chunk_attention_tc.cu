@@ -31,9 +31,14 @@
 // after next.  Scores of 128 keys at once into one buffer, their weights in
 // halves, the tiles taking turns, were slower (903 us: the softmax waits for each round).  One
 // issuing thread for both tiles under `lane == 0` issued at 70 cycles a product (1001 us).
-// With codes the same work takes 890 us: the conversion's instructions
-// and loads lengthen the softmax from 870 to 1400 cycles a step; neither deeper loads,
-// fewer instructions in the conversion nor other register shares changed that.
+// With codes the same work takes 752 us, and 64 sequences of 16 rows 246 us against
+// 229 in bf16: a step of two tiles takes 1600 cycles in place of 1390, for the four
+// converting warps share the issue slots and the instruction cache with the softmax (without its
+// exponentials a step takes as long).  What helped is less code and fewer instructions:
+// the next codes are asked for only when the last are published (64 x 16 rows 260 -> 249 us),
+// stores that need no swap (280 -> 260), short loops at an item's ends (315 -> 283),
+// no spilled register (a few in the conversion cost 50 us).  What did not: eight converting
+// warps, codes by bulk copies through shared memory, blocks of 64 keys.
 //
 #include "chunk.cuh"
 #include "tcgen05.cuh"
@@ -71,7 +76,7 @@ struct Cfg {
   static constexpr int FULL_COUNT = kCodes ? 4 : 1;
   // registers a thread: softmax, products and copies, conversion (launched with
   // 65536 / THREADS, rounded down to a multiple of 8: 168, or 128)
-  static constexpr int R_SOFT = kCodes ? 176 : 192, R_ISSUE = kCodes ? 48 : 120, R_CONV = 112;
+  static constexpr int R_SOFT = kCodes ? 168 : 192, R_ISSUE = kCodes ? 64 : 120, R_CONV = 112;
   static_assert(2 * R_SOFT + R_ISSUE + (kCodes ? R_CONV : 0) <= (kCodes ? 4 * 128 : 3 * 168), "register shares");
   static constexpr int T_O = 2 * BK;                  // TMEM columns of O_0
 };
@@ -241,11 +246,12 @@ __device__ __forceinline__ Tile make_tile(const SeqRows& s, const Item& it, int 
 }
 
 // What a block of the item costs, and an item before its first block (query,
-// first scores, output), in eighths of a block of two tiles: measured, a block
-// of one tile takes 2450 cycles against 2750 and an item begins at 3.7 blocks.
-// (With every block alike the SMs with the short items ended last: 4096 new tokens 193 us.)
+// first scores, output), in eighths of a block of two tiles: a block
+// of one tile takes 2450 cycles against 2750; items at 3 blocks were the fastest of
+// 3 to 5.5 (six prompts 82 us, 84 at 4.5).
+// (With every block alike the SMs with the short items ended last: 4096 new tokens 193 us, now 120.)
 __device__ __forceinline__ int weight(const Item& it) { return it.rows > BM ? 8 : 7; }
-constexpr int kItemCost = 36;
+constexpr int kItemCost = 24;
 __device__ __forceinline__ int units_of(const Item& it) { return kItemCost + it.blocks * weight(it); }
 
 // A part of a run: blocks [b0, b1) of an item of (sequence b, key head h) whose first unit is u0.
@@ -569,10 +575,13 @@ __global__ void __launch_bounds__(Cfg<D, FMT>::THREADS, 1)
       } else {
         // A warp takes two pages of the block's eight: 8 lanes (4 with 64 columns)
         // a row, 16 codes each.  K and V have registers of their own, asked for
-        // again (for the next block) as soon as they are stored, so two tiles are
-        // on their way at any time; a lane holds the scale of one of the 32 rows.
+        // again (for the next block) as soon as their products may start; a lane
+        // holds the scale of one of the 32 rows.
         constexpr int LANES = D / 16, RP = kWarp / LANES, NR = kWarp / RP;  // rows a pass, passes
-        const int cw = warp - CONV_WARP, ch = lane % LANES, sub = lane / LANES;
+        const int cw = warp - CONV_WARP;
+        // this lane's codes [16 ch, + 16) of row sub of a pass: 8 lanes take 64 codes of an even
+        // and of an odd row, whose swizzled chunks share no bank when they are stored
+        const int ch = D == 128 ? (lane & 3) | ((lane >> 1) & 4) : lane & 3, sub = D == 128 ? ((lane >> 2) & 1) | ((lane >> 3) & 2) : lane >> 2;
         const uint32_t page_bytes = static_cast<uint32_t>(n_kv) * 2 * kPage * D, page_scales = static_cast<uint32_t>(n_kv) * 2 * kPage;
         uint4 w[2][NR];
         uint32_t sc[2];
@@ -590,17 +599,21 @@ __global__ void __launch_bounds__(Cfg<D, FMT>::THREADS, 1)
           if (r >= rows.x && r < rows.y) sc[kv] = p.c.scales[(unsigned long long)page * page_scales + (h * 2 + kv) * kPage + (lane & 15)];
           return rows;
         };
-        auto ask = [&](int2 rows, int kv, int i) {
-          const int r = cw * kWarp + i * RP + sub;
-          w[kv][i] = make_uint4(0u, 0u, 0u, 0u);
-          if (r >= rows.x && r < rows.y) w[kv][i] = load16(reinterpret_cast<const uint4*>(from[i * RP >> 4] + (i * RP & 15) * D));
+        auto ask = [&](int2 rows, int kv) {
+          if (rows.x <= cw * kWarp && rows.y >= (cw + 1) * kWarp) {
+#pragma unroll
+            for (int i = 0; i < NR; ++i) w[kv][i] = load16(reinterpret_cast<const uint4*>(from[i * RP >> 4] + (i * RP & 15) * D));
+          } else {
+#pragma unroll
+            for (int i = 0; i < NR; ++i) {
+              const int r = cw * kWarp + i * RP + sub;
+              w[kv][i] = make_uint4(0u, 0u, 0u, 0u);
+              if (r >= rows.x && r < rows.y) w[kv][i] = load16(reinterpret_cast<const uint4*>(from[i * RP >> 4] + (i * RP & 15) * D));
+            }
+          }
         };
 #pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-          const int2 rows = ask_rows(0, kv);
-#pragma unroll
-          for (int i = 0; i < NR; ++i) ask(rows, kv, i);
-        }
+        for (int kv = 0; kv < 2; ++kv) ask(ask_rows(0, kv), kv);
         for (int jj = 0; jj < n; ++jj) {
           if (((jj + 1) & 3) == 0) {
             ids = ids_next;
@@ -613,10 +626,8 @@ __global__ void __launch_bounds__(Cfg<D, FMT>::THREADS, 1)
             // 2^e in fp16, below its normal range for e = -15
             const uint32_t bits = sc[kv] == 112 ? 0x200u : (sc[kv] - 112) << 10;
             const uint32_t pair = bits | (bits << 16);
-            int2 rows = make_int2(0, 0);
-            if (jj + 1 < n) rows = ask_rows(jj + 1, kv);
             uint8_t* dst = smem + slot * C::SLOT + (ch >> 2) * HALF;
-            const int c0 = (ch & 3) * 2, f = (ch >> 2) & 1;  // upper halves store their second chunk first: no bank meets twice
+            const int c0 = (ch & 3) * 2;
 #pragma unroll
             for (int i = 0; i < NR; ++i) {
               const int r = cw * kWarp + i * RP + sub;
@@ -631,14 +642,13 @@ __global__ void __launch_bounds__(Cfg<D, FMT>::THREADS, 1)
                 o[x] = *reinterpret_cast<const uint32_t*>(&y);
               }
               uint8_t* row = dst + r * 128;
-              const uint4 a = make_uint4(o[0], o[1], o[2], o[3]), c = make_uint4(o[4], o[5], o[6], o[7]);
-              *reinterpret_cast<uint4*>(row + (((c0 + f) ^ (r & 7)) << 4)) = f ? c : a;
-              *reinterpret_cast<uint4*>(row + (((c0 + 1 - f) ^ (r & 7)) << 4)) = f ? a : c;
-              ask(rows, kv, i);
+              *reinterpret_cast<uint4*>(row + ((c0 ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+              *reinterpret_cast<uint4*>(row + (((c0 + 1) ^ (r & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
             }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&full[slot]);
+            if (jj + 1 < n) ask(ask_rows(jj + 1, kv), kv);
             next();
           }
         }
@@ -784,7 +794,7 @@ __global__ void __launch_bounds__(Cfg<D, FMT>::THREADS, 1)
         // this row's query into the tile (its last readers are done: the scores were all seen)
         // the warp's 32 rows, D / 8 lanes a row.  (Short loops here and in the
         // output: this code runs once an item, and unrolled it was fetched
-        // anew each time, 9000 cycles where the copies take 2000.)
+        // anew each time: 9500 cycles an item where this takes 6000.)
         constexpr int QL = D / 8, QR = kWarp / QL;  // lanes a row, rows a pass
         const long long mine = in_next ? (long long)(s.off + row / group) * p.q_stride + (long long)(part.h * group + row % group) * D : -1;
         const int ch = lane % QL, sub = lane / QL;
