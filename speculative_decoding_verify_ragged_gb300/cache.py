@@ -66,8 +66,7 @@ class PagedCache:
         self.workspace = torch.empty(int(nbytes), dtype=torch.uint8, device="cuda")
         self.device = self.workspace.device
         self._index = self.workspace.get_device()
-        self._append_rows = SdvAppendRows()
-        self._append_ref = ctypes.byref(self._append_rows)
+        self._n_q, self._n_kv, self._d = self.cfg.n_q, self.cfg.n_kv, self.cfg.head_dim
         h = ctypes.c_void_p()
         self._check(self.lib.sdv_cache_create(ctypes.byref(self.cfg), _ptr(self.workspace), ctypes.c_size_t(nbytes),
                                               self.max_rows, self.max_slots, _stream(None), ctypes.byref(h)),
@@ -102,7 +101,7 @@ class PagedCache:
 
     def _rows(self, t, name, heads, rows, dtypes):
         """The row stride of a [>= rows, heads, head_dim] tensor whose heads are contiguous."""
-        d = self.cfg.head_dim
+        d = self._d
         n, st = t.shape, t.stride()
         if len(n) == 3 and t.dtype in dtypes and t.get_device() == self._index and n[0] >= rows and n[1] == heads \
                 and n[2] == d and st[2] == 1 and (st[1] == d or heads == 1):
@@ -155,27 +154,25 @@ class PagedCache:
     def append(self, chunk: Chunk, k, v, status, q=None, q_out=None, stream=None):
         """Store the chunk's k, v [T, n_kv, head_dim] (bf16 or fp32, rows strided), rotated where the cache
         rotates; with q [T, n_q, head_dim] also its rotation in bf16 into q_out."""
-        c, T, r = self.cfg, chunk.rows, self._append_rows
-        io = (k.dtype,)
-        r.k_stride = self._rows(k, "k", c.n_kv, T, BOTH)
-        r.v_stride = self._rows(v, "v", c.n_kv, T, io)
-        r.k, r.v, r.x_format = k.data_ptr(), v.data_ptr(), 1 if k.dtype is torch.float32 else 0
-        if q is None and q_out is None:
-            r.q = r.q_out = None
-        elif q is None or q_out is None:
+        n_kv, T, x = self._n_kv, chunk.rows, k.dtype
+        io = (x,)
+        ks, vs = self._rows(k, "k", n_kv, T, BOTH), self._rows(v, "v", n_kv, T, io)
+        qp = op = None
+        qs = os_ = 0
+        if q is not None and q_out is not None:
+            qs, qp = self._rows(q, "q", self._n_q, T, io), q.data_ptr()
+            os_, op = self._rows(q_out, "q_out", self._n_q, T, BF16), q_out.data_ptr()
+        elif q is not None or q_out is not None:
             raise ValueError("q and q_out come together")
-        else:
-            r.q_stride = self._rows(q, "q", c.n_q, T, io)
-            r.q_out_stride = self._rows(q_out, "q_out", c.n_q, T, BF16)
-            r.q, r.q_out = q.data_ptr(), q_out.data_ptr()
+        r = SdvAppendRows(k.data_ptr(), v.data_ptr(), qp, ks, vs, qs, 1 if x is torch.float32 else 0, op, os_)
         st, raw = self._enqueue(status, stream)
-        rc = self.lib.sdv_cache_append(self.handle, chunk.ref, self._append_ref, st, raw)
+        rc = self.lib.sdv_cache_append(self.handle, chunk.ref, ctypes.byref(r), st, raw)
         if rc:
             self._check(rc, "sdv_cache_append")
 
     def attention(self, chunk: Chunk, q, out, status, stream=None):
         """Attention of q [T, n_q, head_dim] bf16 over the cached positions each row sees, into out."""
-        n_q, T = self.cfg.n_q, chunk.rows
+        n_q, T = self._n_q, chunk.rows
         qs, os_ = self._rows(q, "q", n_q, T, BF16), self._rows(out, "out", n_q, T, BF16)
         st, raw = self._enqueue(status, stream)
         rc = self.lib.sdv_cache_attention(self.handle, chunk.ref, q.data_ptr(), qs, out.data_ptr(), os_, st, raw)
@@ -184,7 +181,7 @@ class PagedCache:
 
     def read(self, chunk: Chunk, k_out, v_out, status, stream=None):
         """Read the chunk's positions back into k_out, v_out [T, n_kv, head_dim] (bf16 or fp32; either may be None)."""
-        n_kv, T = self.cfg.n_kv, chunk.rows
+        n_kv, T = self._n_kv, chunk.rows
         first = k_out if k_out is not None else v_out
         if first is None:
             raise ValueError("k_out, v_out: one of them is wanted")
