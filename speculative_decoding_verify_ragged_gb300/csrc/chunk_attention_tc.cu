@@ -25,7 +25,7 @@
 //
 // What bounds it, 32 query and 8 key heads of 128, bf16: 2048 new tokens over 32749
 // take 665 us in a graph's replays (1600 TFLOP/s, 0.84 of the burst peak, 0.94 of the sustained one; back
-// to back for long the power limit holds it at 740 us).  A block of two tiles takes 3060 cycles: its
+// to back for long the power limit holds it at 732 us).  A block of two tiles takes 2780 cycles: its
 // products 2560 (N = 64 scores wait for shared memory: 48 cycles each in place
 // of 32, measured), the rest is the round from a step's weights to the scores
 // after next.  Scores of 128 keys at once into one buffer, their weights in
@@ -39,7 +39,6 @@
 // stores that need no swap (280 -> 260), short loops at an item's ends (315 -> 283),
 // no spilled register (a few in the conversion cost 50 us).  What did not: eight converting
 // warps, codes by bulk copies through shared memory, blocks of 64 keys.
-//
 #include "chunk.cuh"
 #include "tcgen05.cuh"
 
@@ -921,6 +920,8 @@ __global__ void __launch_bounds__(Cfg<D, FMT>::THREADS, 1)
         const float inv = l == 0.f ? 0.f : 1.f / l;  // a row that sees nothing gives 0
         const long long out_at = write ? (long long)(e.off + e_row / group) * p.out_stride + (long long)(e.h * group + e_row % group) * D : -1;
         if (others == 0 || __any_sync(0xffffffffu, join && write)) {
+          // unrolled, the other parts' loads overlap (six prompts, bf16: 84 us against 88); over codes the
+          // longer code costs more than that (107 against 101)
 #pragma unroll(C::kCodes ? 1 : D / 32)
           for (int c = 0; c < D / 32; ++c) {
             uint32_t r[32];
