@@ -33,7 +33,13 @@ constexpr int CA_THREADS = CA_WARPS * kWarp;
 constexpr float kNoMax = -1e30f;  // the maximum before the first visible key
 constexpr int kFewItems = 4;      // blocks per item from which the items are cut by themselves (2, 3, 4: 18 sequences 33.4, 33.5, 32.6 us)
 constexpr int kMinPages = 4;      // pages a block takes at least: one per warp (4, 8, 16: 11.5, 11.8, 13.3 us for one sequence of 517)
-constexpr int kSplitBias = 8;     // e4m3: weights carry 2^(e + 8), in fp16's normal range for every e
+// e4m3: a weight enters fp16 times its value's scale, 2^(s + e), and the bound m is one of s + e: the largest
+// stands at 2^15, so weights keep fp16's half step of 2^-11 down to 2^-29 of the largest, whatever e is.  A page whose
+// own largest lies more than 24 binades down moves the bound there (sum and output scale up; they are fp32),
+// so that one key far above the rest takes nothing from the pages behind it.  A bound is moved down by 48 binades at
+// most, and no more once the sum is past 2^50 (sums stay below 2^101, outputs below 2^117): what is lost
+// then is below 2^-50 of the sum.
+constexpr float kTopWeight = 15.f, kDeepest = 24.f, kSumMost = 0x1p50f, kDropMost = 48.f;
 
 constexpr int part_floats(int D) { return kItemRows * (D + 2); }
 
@@ -350,19 +356,25 @@ __global__ void __launch_bounds__(CA_THREADS, per_sm<D, FMT, NT>()) chunk_attn_k
           for (int r = 0; r < NT; ++r) mma_bf16(s[r], a, qf[r][ks][0], qf[r][ks][1]);
         }
       }
-      // base-2 logits
-      float vs[2] = {1.f, 1.f};
+      // base-2 logits; e4m3: plus the exponent e of the value's scale, and 2^-e for the sum
+      float un[2] = {1.f, 1.f};
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
-        float ksc = 1.f;
         if constexpr (F::kCodes) {
-          ksc = scale_value(cur.sc[y]);
-          vs[y] = scale_value((cur.sc[y] >> 8) + kSplitBias);
-        }
+          const uint32_t vb = cur.sc[y] >> 8;
+          const float ksc = scale_value(cur.sc[y]), ve = __uint_as_float(0x4B000000u | vb) - 8388735.f;  // 2^23 + byte, less 2^23 + 127
+          un[y] = scale_value(254u - vb);
 #pragma unroll
-        for (int r = 0; r < NT; ++r) {
-          s[r][2 * y] *= cz[r][0] * ksc;
-          s[r][2 * y + 1] *= cz[r][1] * ksc;
+          for (int r = 0; r < NT; ++r) {
+            s[r][2 * y] = fmaf(s[r][2 * y], cz[r][0] * ksc, ve);
+            s[r][2 * y + 1] = fmaf(s[r][2 * y + 1], cz[r][1] * ksc, ve);
+          }
+        } else {
+#pragma unroll
+          for (int r = 0; r < NT; ++r) {
+            s[r][2 * y] *= cz[r][0];
+            s[r][2 * y + 1] *= cz[r][1];
+          }
         }
       }
       const bool full = key0 + kPage - 1 <= pmin && (window <= 0 || key0 > pmax - window);
@@ -372,7 +384,7 @@ __global__ void __launch_bounds__(CA_THREADS, per_sm<D, FMT, NT>()) chunk_attn_k
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
           const int key = key0 + g + 8 * y;
-          if (key > pmax || (window > 0 && key <= pmin - window)) vs[y] = 0.f;
+          if (key > pmax || (window > 0 && key <= pmin - window)) un[y] = 0.f;
 #pragma unroll
           for (int r = 0; r < NT; ++r)
 #pragma unroll
@@ -387,17 +399,38 @@ __global__ void __launch_bounds__(CA_THREADS, per_sm<D, FMT, NT>()) chunk_attn_k
             for (int w = 0; w < F::VW; ++w) cur.v[r][w] = 0u;
         }
       }
-      bool up = false;
+      bool move = false;
 #pragma unroll
-      for (int r = 0; r < NT; ++r) up |= fmaxf(s[r][0], s[r][2]) > m[r][0] || fmaxf(s[r][1], s[r][3]) > m[r][1];
-      if (__any_sync(0xffffffffu, up)) {
+      for (int r = 0; r < NT; ++r)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const float top = fmaxf(s[r][x], s[r][2 + x]);
+          if constexpr (F::kCodes) {
+            const float a = top - m[r][x];
+            move |= a > kTopWeight || (a < kTopWeight - kDeepest && top > kNoMax);
+          } else {
+            move |= top > m[r][x];
+          }
+        }
+      if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
         for (int r = 0; r < NT; ++r)
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            float top = fmaxf(fmaxf(s[r][x], s[r][2 + x]), m[r][x]);
+            float top = fmaxf(s[r][x], s[r][2 + x]);
+            if constexpr (!F::kCodes) top = fmaxf(top, m[r][x]);
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+            if constexpr (F::kCodes) {
+              // the page's largest decides; every lane of the row comes to the same bound
+              float most = l[r][x];
+#pragma unroll
+              for (int d = 4; d < 32; d <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
+              const bool seen = top > kNoMax;
+              top -= kTopWeight;
+              const float old = m[r][x];
+              if (!(top > old)) top = seen && top < old - kDeepest && most <= kSumMost ? fmaxf(top, old - kDropMost) : old;
+            }
             const float f = fast_ex2(m[r][x] - top);
             m[r][x] = top;
             l[r][x] *= f;
@@ -411,13 +444,15 @@ __global__ void __launch_bounds__(CA_THREADS, per_sm<D, FMT, NT>()) chunk_attn_k
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
           const float a = fast_ex2(s[r][2 * y] - m[r][0]), b2 = fast_ex2(s[r][2 * y + 1] - m[r][1]);
-          l[r][0] += a;
-          l[r][1] += b2;
           uint32_t w;
           if constexpr (F::kCodes) {
-            const __half2 hw = __floats2half2_rn(a * vs[y], b2 * vs[y]);
+            l[r][0] = fmaf(a, un[y], l[r][0]);
+            l[r][1] = fmaf(b2, un[y], l[r][1]);
+            const __half2 hw = __floats2half2_rn(a, b2);
             w = *reinterpret_cast<const uint32_t*>(&hw);
           } else {
+            l[r][0] += a;
+            l[r][1] += b2;
             w = pack_bf16x2(a, b2);
           }
           pb[r][y] = transpose8(w);
@@ -445,7 +480,6 @@ __global__ void __launch_bounds__(CA_THREADS, per_sm<D, FMT, NT>()) chunk_attn_k
     }
 
     // the warps' parts into shared memory, then joined
-    const float undo = F::kCodes ? 1.f / (1 << kSplitBias) : 1.f;
 #pragma unroll
     for (int r = 0; r < NT; ++r)
 #pragma unroll
@@ -460,7 +494,7 @@ __global__ void __launch_bounds__(CA_THREADS, per_sm<D, FMT, NT>()) chunk_attn_k
 #pragma unroll
         for (int j = 0; j < F::MT; ++j)
           *reinterpret_cast<float2*>(s_o + (warp * ROWS + row) * D + out_col<D, FMT>(g, j)) =
-              make_float2(o[r][j][x] * undo, o[r][j][2 + x] * undo);
+              make_float2(o[r][j][x], o[r][j][2 + x]);
       }
     __syncthreads();
     constexpr int TPR = CA_THREADS / ROWS, PER = D / TPR;  // threads a row, columns a thread
