@@ -8,6 +8,8 @@ tests/cache_helpers.py counts for every row, the weights that fall below fp16's 
 
 Few rows (mma.sync): a weight goes in times its value's scale 2^e.  On the first page of a row its largest such product
 stands at 2^15, so the unit is 2^-15 of it; on every later page the largest is at least 2^-9 units.
+Many rows (tcgen05): steps of 64 keys.  The first step's largest weight stands at 2^4, and every later step's
+weights add up to at least 2^-8 units.
 """
 import math
 
@@ -46,13 +48,14 @@ def _sunk(q_len, kv, gap, size, seed):
     return s, exps[1].double()
 
 
-def _bound(s, e):
-    """(out, how far it may be off): the weights by pages of 16 keys."""
+def _bound(s, e, few):
+    """(out, how far it may be off): the weights by blocks of 16 keys (few rows) or 64."""
     n, kv = s["q_lens"][0], s["kv_lens"][0]
     out = torch.zeros((n, N_Q, D), dtype=torch.float64, device="cuda")
     tol = torch.zeros_like(out)
     at, pos = torch.arange(kv, device="cuda"), ch.positions(s, 0)
     see = at[None] <= pos[:, None]
+    width = 16 if few else 64
     for j in range(N_Q):
         k, v = ch.cached(s, 0, j // 2)
         q = s["q"][:, j].double()
@@ -62,17 +65,23 @@ def _bound(s, e):
         size = ((q.abs() @ k.abs().T) / math.sqrt(D)).masked_fill(~see, 0).amax(-1, keepdim=True)
         tol[:, j] = (p @ v.abs()) * (ch.FP16_HALF + 2 * (D * 2.0 ** -23 * size + 2.0 ** -20)) + ch.BF16_HALF * out[:, j].abs()
         scale = torch.exp2(e[:, j // 2])
-        for b0 in range(0, kv, 16):
-            b = slice(b0, min(kv, b0 + 16))
-            unit = (p[:, b] * scale[b]).amax(-1, keepdim=True) * (2.0 ** -15 if b0 == 0 else 2.0 ** 9)
-            tol[:, j] += 2.0 ** -25 * unit * (v[b].abs() / scale[b][:, None]).sum(0)   # the codes' magnitudes
+        for b0 in range(0, kv, width):
+            b = slice(b0, min(kv, b0 + width))
+            if few:    # against codes: v / scale
+                top = (p[:, b] * scale[b]).amax(-1, keepdim=True)
+                unit = top * (2.0 ** -15 if b0 == 0 else 2.0 ** 9)
+                small = (v[b].abs() / scale[b][:, None]).sum(0)
+            else:
+                unit = p[:, b].amax(-1, keepdim=True) * 2.0 ** -4 if b0 == 0 else p[:, b].sum(-1, keepdim=True) * 2.0 ** 8
+                small = v[b].abs().sum(0)
+            tol[:, j] += 2.0 ** -25 * unit * small
     return out, tol
 
 
-def _check(rows, size, gap, copies):
+def _check(rows, size, gap, copies, few):
     from speculative_decoding_verify_ragged_gb300.cache import PagedCache
     s, e = _sunk(rows, 4096 + rows, gap, size, seed=rows + gap)
-    want, tol = _bound(s, e)
+    want, tol = _bound(s, e, few)
     c = PagedCache(dict(n_q=N_Q, n_kv=N_KV, head_dim=D, cache_format="e4m3"), max_rows=rows * copies, max_slots=copies)
     q = s["q"].repeat(copies, 1, 1)
     out = torch.full_like(q, 7.0)
@@ -92,4 +101,12 @@ def _check(rows, size, gap, copies):
 @pytest.mark.parametrize("size", [0.1, 0.01, 0.003])
 @pytest.mark.parametrize("gap", [10, 12, 14, 16])
 def test_few_rows_beside_a_sink(rows, size, gap, copies):
-    _check(rows, size, gap, copies)
+    _check(rows, size, gap, copies, True)
+
+
+@pytest.mark.parametrize("copies", [1, 160])
+@pytest.mark.parametrize("rows", [9, 64, 200])     # 18, 128 and 400 packed rows
+@pytest.mark.parametrize("size", [0.1, 0.01])
+@pytest.mark.parametrize("gap", [10, 12, 14, 16, 18])
+def test_many_rows_beside_a_sink(rows, size, gap, copies):
+    _check(rows, size, gap, copies, False)
