@@ -15,7 +15,7 @@ Typical use, a chunk of new tokens through one layer::
 
 A chunk keeps the addresses of its tensors; their contents (offsets, lengths,
 tables, pages) may change between calls, so one chunk serves a captured graph
-or a loop of steps.
+or a loop of steps, and every cache of the same key heads, head size and format.
 """
 from __future__ import annotations
 
@@ -33,10 +33,11 @@ FORMATS = {"bf16": SDV_CACHE_BF16, "e4m3": SDV_CACHE_E4M3}
 
 
 class Chunk:
-    """A ragged chunk's description (sdv_chunk) and the tensors that it points to."""
+    """A ragged chunk's description (sdv_chunk), the tensors that it points to and the geometry of their pages."""
 
-    def __init__(self, struct: SdvChunk, tensors: tuple):
+    def __init__(self, struct: SdvChunk, tensors: tuple, geometry: tuple):
         self.struct = struct
+        self.geometry = geometry
         self.ref = ctypes.byref(struct)
         self.rows = struct.T
         self.tensors = tensors
@@ -56,22 +57,25 @@ class PagedCache:
         fmt = cfg.get("cache_format", "bf16")
         if fmt not in FORMATS:
             raise ValueError(f"cache_format {fmt!r}: one of {sorted(FORMATS)}")
-        self.format = fmt
-        self.cfg = SdvCacheConfig(int(cfg["n_q"]), int(cfg["n_kv"]), int(cfg["head_dim"]),
-                                  int(cfg.get("page_size", 16)), FORMATS[fmt], float(cfg.get("rope_theta", 0.0)))
+        c = SdvCacheConfig(int(cfg["n_q"]), int(cfg["n_kv"]), int(cfg["head_dim"]), int(cfg.get("page_size", 16)),
+                           FORMATS[fmt], float(cfg.get("rope_theta", 0.0)))
         self.max_rows, self.max_slots = int(max_rows), int(max_slots)
-        nbytes = self.lib.sdv_cache_workspace_size(ctypes.byref(self.cfg), self.max_rows, self.max_slots)
+        nbytes = self.lib.sdv_cache_workspace_size(ctypes.byref(c), self.max_rows, self.max_slots)
         if nbytes == 0:
             raise SdvError(1, "sdv_cache_workspace_size rejected the configuration")
-        self.workspace = torch.empty(int(nbytes), dtype=torch.uint8, device="cuda")
-        self.device = self.workspace.device
-        self._index = self.workspace.get_device()
-        self._n_q, self._n_kv, self._d = self.cfg.n_q, self.cfg.n_kv, self.cfg.head_dim
+        self._setup(c, fmt, torch.empty(int(nbytes), dtype=torch.uint8, device="cuda"))
         h = ctypes.c_void_p()
         self._check(self.lib.sdv_cache_create(ctypes.byref(self.cfg), _ptr(self.workspace), ctypes.c_size_t(nbytes),
                                               self.max_rows, self.max_slots, _stream(None), ctypes.byref(h)),
                     "sdv_cache_create")
         self.handle = h
+
+    def _setup(self, cfg: SdvCacheConfig, fmt: str, workspace):
+        self.cfg, self.format, self.workspace = cfg, fmt, workspace
+        self.device = workspace.device
+        self._index = workspace.get_device()
+        self._n_q, self._n_kv, self._d = cfg.n_q, cfg.n_kv, cfg.head_dim
+        self._geometry = (cfg.n_kv, cfg.head_dim, fmt, self._index)
 
     def close(self):
         if getattr(self, "handle", None):
@@ -114,6 +118,13 @@ class PagedCache:
             raise ValueError(f"{name}: shape {tuple(n)}, [{rows}, {heads}, {d}] is wanted")
         raise ValueError(f"{name}: strides {tuple(st)}: a row's heads must be contiguous")
 
+    def _mine(self, chunk):
+        """The chunk's rows; its pages must be laid out as this cache's."""
+        if chunk.geometry != self._geometry:
+            raise ValueError(f"chunk: of a cache with (n_kv, head_dim, format, device) {chunk.geometry}, "
+                             f"{self._geometry} is wanted")
+        return chunk.rows
+
     def _enqueue(self, status, stream):
         """The status word's address and the stream's handle (the current stream's by default)."""
         if status.dtype is not torch.int32 or status.get_device() != self._index:
@@ -147,14 +158,14 @@ class PagedCache:
         s = SdvChunk(B, int(rows), int(max_q), row_offsets.data_ptr(), kv_lens.data_ptr(), kv_pool.data_ptr(),
                      kv_scales.data_ptr() if kv_scales is not None else None, int(kv_pool.shape[0]),
                      page_table.data_ptr(), int(page_table.shape[1]), int(window))
-        return Chunk(s, (row_offsets, kv_lens, page_table, kv_pool, kv_scales))
+        return Chunk(s, (row_offsets, kv_lens, page_table, kv_pool, kv_scales), self._geometry)
 
     # -- entry points ------------------------------------------------------
 
     def append(self, chunk: Chunk, k, v, status, q=None, q_out=None, stream=None):
         """Store the chunk's k, v [T, n_kv, head_dim] (bf16 or fp32, rows strided), rotated where the cache
         rotates; with q [T, n_q, head_dim] also its rotation in bf16 into q_out."""
-        n_kv, T, x = self._n_kv, chunk.rows, k.dtype
+        n_kv, T, x = self._n_kv, self._mine(chunk), k.dtype
         io = (x,)
         ks, vs = self._rows(k, "k", n_kv, T, BOTH), self._rows(v, "v", n_kv, T, io)
         qp = op = None
@@ -172,7 +183,7 @@ class PagedCache:
 
     def attention(self, chunk: Chunk, q, out, status, stream=None):
         """Attention of q [T, n_q, head_dim] bf16 over the cached positions each row sees, into out."""
-        n_q, T = self._n_q, chunk.rows
+        n_q, T = self._n_q, self._mine(chunk)
         qs, os_ = self._rows(q, "q", n_q, T, BF16), self._rows(out, "out", n_q, T, BF16)
         st, raw = self._enqueue(status, stream)
         rc = self.lib.sdv_cache_attention(self.handle, chunk.ref, q.data_ptr(), qs, out.data_ptr(), os_, st, raw)
@@ -181,7 +192,7 @@ class PagedCache:
 
     def read(self, chunk: Chunk, k_out, v_out, status, stream=None):
         """Read the chunk's positions back into k_out, v_out [T, n_kv, head_dim] (bf16 or fp32; either may be None)."""
-        n_kv, T = self._n_kv, chunk.rows
+        n_kv, T = self._n_kv, self._mine(chunk)
         first = k_out if k_out is not None else v_out
         if first is None:
             raise ValueError("k_out, v_out: one of them is wanted")
