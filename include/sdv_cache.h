@@ -46,7 +46,8 @@ typedef struct {
 } sdv_cache_config;
 
 /* A ragged chunk of new tokens.
- *  B, T (host)      sequences; rows that the caller's row buffers hold.
+ *  B, T (host)      sequences, at least one; rows that the caller's row buffers hold.  With T = 0 a
+ *                   call enqueues nothing and its row pointers may be null.
  *  max_q (host)     an upper bound of every sequence's rows.
  *  row_offsets [B+1] (device) row_offsets[0] = 0, non-decreasing, row_offsets[B] <= T:
  *                   sequence b owns rows [row_offsets[b], row_offsets[b+1]).

@@ -157,6 +157,7 @@ extern "C" sdv_status sdv_cache_append(sdv_cache* h, const sdv_chunk* chunk, con
   sdv_status rc = chunk_params(h, chunk, status, &p.c);
   if (rc != SDV_OK) return rc;
   if (!rows || (rows->x_format != 0 && rows->x_format != 1)) return SDV_ERR_INVALID_ARG;
+  if (chunk->T == 0) return SDV_OK;  // no rows: their pointers may be null
   const int bytes = rows->x_format ? 4 : 2, d = h->cfg.head_dim;
   const long long kw = (long long)h->cfg.n_kv * d, qw = (long long)h->cfg.n_q * d;
   if ((rc = rows_ok(rows->k, rows->k_stride, kw, bytes)) != SDV_OK) return rc;
@@ -166,7 +167,6 @@ extern "C" sdv_status sdv_cache_append(sdv_cache* h, const sdv_chunk* chunk, con
     if ((rc = rows_ok(rows->q, rows->q_stride, qw, bytes)) != SDV_OK) return rc;
     if ((rc = rows_ok(rows->q_out, rows->q_out_stride, qw, 2)) != SDV_OK) return rc;
   }
-  if (chunk->T == 0) return SDV_OK;
   p.k = rows->k;
   p.v = rows->v;
   p.q = rows->q;
@@ -183,12 +183,11 @@ extern "C" sdv_status sdv_cache_attention(sdv_cache* h, const sdv_chunk* chunk, 
                                           long long out_stride, int* status, void* stream) {
   ChunkAttnParams p;
   sdv_status rc = chunk_params(h, chunk, status, &p.c);
-  if (rc != SDV_OK) return rc;
+  if (rc != SDV_OK || chunk->T == 0) return rc;
   const int d = h->cfg.head_dim;
   const long long qw = (long long)h->cfg.n_q * d;
   if ((rc = rows_ok(q, q_stride, qw, 2)) != SDV_OK) return rc;
   if ((rc = rows_ok(out, out_stride, qw, 2)) != SDV_OK) return rc;
-  if (chunk->T == 0) return SDV_OK;
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.out = static_cast<__nv_bfloat16*>(out);
   p.q_stride = q_stride;
@@ -231,12 +230,12 @@ extern "C" sdv_status sdv_cache_read(sdv_cache* h, const sdv_chunk* chunk, void*
   sdv_status rc = chunk_params(h, chunk, status, &p.c);
   if (rc != SDV_OK) return rc;
   if (out_format != 0 && out_format != 1) return SDV_ERR_INVALID_ARG;
+  if (chunk->T == 0) return SDV_OK;
   const int bytes = out_format ? 4 : 2;
   const long long kw = (long long)h->cfg.n_kv * h->cfg.head_dim;
   if (!k_out && !v_out) return SDV_ERR_INVALID_ARG;
   if (k_out && (rc = rows_ok(k_out, k_stride, kw, bytes)) != SDV_OK) return rc;
   if (v_out && (rc = rows_ok(v_out, v_stride, kw, bytes)) != SDV_OK) return rc;
-  if (chunk->T == 0) return SDV_OK;
   p.k = k_out;
   p.v = v_out;
   p.k_stride = k_stride;
