@@ -17,10 +17,7 @@
 // with its own activation tile tg * cs + r of about R / cs rows, so the
 // weights cross HBM once.  The group's CTAs walk the same units at the same
 // pace, and the first to ask for a weight line brings it into L2 for the
-// others.  (A thread-block cluster sharing the tile by TMA multicast -- two
-// CTAs each load one 64-row half into every CTA of the cluster, and a stage
-// is refilled only once every CTA has released it -- measured the same; it
-// stays selectable for A/B timing.)
+// others.
 //
 // From 128 activation rows the CTAs work in pairs (a cluster of two, tcgen05
 // cta_group::2): one MMA of M = 256 weight rows (128 in each CTA's shared
@@ -64,7 +61,7 @@ using namespace tc;
 constexpr int TC_THREADS = 10 * kWarp;
 constexpr int EC = 16;           // accumulator columns per tcgen05.ld / epilogue chunk
 constexpr int kMaxStages = 10;
-constexpr int kMaxCluster = 8;   // portable cluster size
+constexpr int kMaxGroup = 8;     // CTAs that share a weight tile, at most
 // staging row stride: eight lanes of a row reading columns sub + 8 i of four
 // consecutive rows hit 32 different banks
 constexpr int EPI_LD = BM + 8;
@@ -101,27 +98,6 @@ __device__ __forceinline__ uint32_t cluster_id_x() {
 // Every thread of every CTA of the cluster.
 __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
-}
-
-// TMA tile load into the same shared-memory offset of every CTA in `mask`,
-// each CTA's barrier at `bar`'s offset receiving the bytes.
-__device__ __forceinline__ void tma_load_2d_mc(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y,
-                                               uint16_t mask, uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster.L2::cache_hint"
-      " [%0], [%1, {%3, %4}], [%2], %5, %6;" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "h"(mask), "l"(policy)
-      : "memory");
-}
-
-// Arrive on the barrier at `bar`'s offset in every CTA of `mask` once every
-// tcgen05 operation issued so far by this thread completes.
-__device__ __forceinline__ void umma_commit_mc(uint64_t* bar, uint16_t mask) {
-  asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-          smem_u32(bar)),
-      "h"(mask)
-      : "memory");
 }
 
 // ---- CTA pairs (tcgen05 cta_group::2) ----
@@ -202,7 +178,6 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
   griddep_launch_dependents();
 
   const int NT = p.nt, S = p.stages, cs = p.cs;
-  const bool mc = !PAIR && p.multicast != 0;  // a cluster shares weight tiles by multicast (else through L2)
   const int STAGE = tc_stage_bytes(NT, XP, PAIR);
   const int NTC = PAIR ? NT / 2 : NT;  // activation rows this CTA loads per stage
   uint8_t* smem = align1024(smem_raw);
@@ -219,15 +194,14 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
   // CTA pairs: half 0 issues the pair's MMAs; the pairs form the groups
   const int half = PAIR ? static_cast<int>(cluster_ctarank()) : 0;
   const int team = PAIR ? static_cast<int>(cluster_id_x()) : static_cast<int>(blockIdx.x);
-  const int rank = mc ? static_cast<int>(cluster_ctarank()) : team % cs;
-  const int q = mc ? static_cast<int>(cluster_id_x()) : team / cs;
+  const int rank = team % cs;
+  const int q = team / cs;
   const int Q = static_cast<int>(gridDim.x) / (PAIR ? 2 * cs : cs);
-  const uint16_t everyone = static_cast<uint16_t>((1u << cs) - 1u);
   const uint32_t ncols = tmem_columns(NT);
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], mc ? cs : 1);  // one release per CTA of a multicast cluster
+      mbar_init(&empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tfull[b], 1);
@@ -254,8 +228,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  // every CTA's barriers exist before a peer's multicast, copy or arrival can land on them
-  if (mc || PAIR) cluster_sync_all();
+  // both CTAs' barriers exist before a peer's copy or arrival can land on them
+  if constexpr (PAIR) cluster_sync_all();
   const uint32_t tmem = *tmem_slot;
   // a pair's stage fills and accumulator releases count on the issuing CTA's barriers
   const uint32_t lead_full = PAIR ? cluster_addr(full, 0) : 0u;
@@ -312,15 +286,11 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         } else if (cs == 1) {
           tma_load_2d_hint(sa, &tmA0, &full[stage], cu.k * BK, rowA0, pol);
           tma_load_2d_hint(sa + A_BYTES / 2, &tmA1, &full[stage], cu.k * BK, rowA1, pol);
-        } else if (!mc) {
+        } else {
           // the group's CTAs read the same weight tile at about the same time:
           // the first brings it into L2 (normal priority), the others hit there
           tma_load_2d(sa, &tmA0, &full[stage], cu.k * BK, rowA0);
           tma_load_2d(sa + A_BYTES / 2, &tmA1, &full[stage], cu.k * BK, rowA1);
-        } else if (rank == 0) {
-          tma_load_2d_mc(sa, &tmA0, &full[stage], cu.k * BK, rowA0, everyone, pol);
-        } else if (rank == 1) {
-          tma_load_2d_mc(sa + A_BYTES / 2, &tmA1, &full[stage], cu.k * BK, rowA1, everyone, pol);
         }
       };
       auto acts = [&](const Cursor& cu, int stage) {
@@ -369,7 +339,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         uint32_t phase = pre == S ? 1u : 0u;
         bool dead = false;
         for (int j = pre; j < my_units; ++j) {
-          // every CTA of the cluster has released this stage
+          // both CTAs of a pair have released this stage
           if (!mbar_wait(&empty[stage], phase ^ 1)) {
             set_status(p.status, SDV_ERR_TIMEOUT);
             dead = true;
@@ -384,7 +354,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
             phase ^= 1;
           }
         }
-        // stay until the MMAs of the whole cluster have released every stage
+        // stay until the MMAs of the whole pair have released every stage
         // (no copy in flight and no release still to arrive at exit)
         for (int i = 0; i < S && !dead; ++i) {
           if (!mbar_wait(&empty[stage], phase ^ 1)) {
@@ -436,9 +406,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                 else umma_bf16(d, a, b, idesc, (k > k0 || kk > 0 || pl > 0) ? 1u : 0u);
               }
             }
-            // frees the stage, in every CTA of the cluster, once these MMAs have read it
+            // frees the stage, in both CTAs of a pair, once these MMAs have read it
             if constexpr (PAIR) umma_commit_pair(&empty[stage]);
-            else if (mc) umma_commit_mc(&empty[stage], everyone);
             else umma_commit(&empty[stage]);
             if (++stage == S) {
               stage = 0;
@@ -605,12 +574,11 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
       }
     }
   }
-  // every role is done: the producer saw every stage released by the whole
-  // cluster, every accumulator has been read; then no peer touches this CTA's
+  // every role is done: the producer saw every stage released, every accumulator has been read; then no peer touches this CTA's
   // shared memory or barriers any more
   tc_fence_before();
   __syncthreads();
-  if (mc || PAIR) cluster_sync_all();
+  if constexpr (PAIR) cluster_sync_all();
   tc_fence_after();
   if (warp == 1) {
     if constexpr (PAIR)
@@ -757,31 +725,16 @@ int pair_mode() {
   return mode;
 }
 
-// How the single CTAs that take different activation tiles of the same weight
-// tile share its read: multicast within a thread-block cluster, or a group of
-// consecutive CTAs reading it at about the same time through L2.
-// SDV_GEMM_SHARE=mc|l2|off in the environment picks one (A/B timing); the
-// default is l2.
-int share_mode() {
-  static const int mode = [] {
-    const char* v = std::getenv("SDV_GEMM_SHARE");
-    if (v && std::strcmp(v, "mc") == 0) return 1;
-    if (v && std::strcmp(v, "off") == 0) return 0;
-    return 2;
-  }();
-  return mode;
-}
-
 int smem_for(int nt, int xp, bool pair = false) {
   return FIXED_BYTES + tc_stages(nt, xp, pair) * tc_stage_bytes(nt, xp, pair);
 }
 
-// How many clusters of `cs` CTAs of this kernel fit on the GPU at once (cached).
-int active_clusters(Kern k, int cs, int smem, int sms, bool hw_cluster) {
+// How many CTA pairs of this kernel fit on the GPU at once (cached).
+int active_pairs(Kern k, int smem, int sms) {
   static std::mutex mu;
   struct Entry {
     Kern k;
-    int dev, cs, smem, n;
+    int dev, smem, n;
   };
   static Entry cache[64];
   static int used = 0;
@@ -790,33 +743,29 @@ int active_clusters(Kern k, int cs, int smem, int sms, bool hw_cluster) {
   {
     std::lock_guard<std::mutex> lock(mu);
     for (int i = 0; i < used; ++i)
-      if (cache[i].k == k && cache[i].dev == dev && cache[i].cs == cs && cache[i].smem == smem) return cache[i].n;
+      if (cache[i].k == k && cache[i].dev == dev && cache[i].smem == smem) return cache[i].n;
   }
   int n = 0;
   if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) == cudaSuccess) {
-    if (cs == 1 || !hw_cluster) {
-      n = sms / cs;
-    } else {
-      cudaLaunchConfig_t cfg = {};
-      cfg.gridDim = dim3(static_cast<unsigned>(sms / cs * cs));
-      cfg.blockDim = dim3(TC_THREADS);
-      cfg.dynamicSmemBytes = static_cast<size_t>(smem);
-      cudaLaunchAttribute attr[1];
-      attr[0].id = cudaLaunchAttributeClusterDimension;
-      attr[0].val.clusterDim.x = static_cast<unsigned>(cs);
-      attr[0].val.clusterDim.y = 1;
-      attr[0].val.clusterDim.z = 1;
-      cfg.attrs = attr;
-      cfg.numAttrs = 1;
-      if (cudaOccupancyMaxActiveClusters(&n, k, &cfg) != cudaSuccess) {
-        (void)cudaGetLastError();
-        n = 0;
-      }
-      if (n * cs > sms) n = sms / cs;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(sms / 2 * 2));
+    cfg.blockDim = dim3(TC_THREADS);
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, k, &cfg) != cudaSuccess) {
+      (void)cudaGetLastError();
+      n = 0;
     }
+    if (n * 2 > sms) n = sms / 2;
   }
   std::lock_guard<std::mutex> lock(mu);
-  if (used < 64) cache[used++] = Entry{k, dev, cs, smem, n};
+  if (used < 64) cache[used++] = Entry{k, dev, smem, n};
   return n;
 }
 
@@ -848,7 +797,7 @@ TcChoice choose_pair(int epi, int xp, const GemmParams& g, int sms, int forced_c
   TcChoice c;
   c.pair = true;
   const int R = g.R;
-  const int pairs = active_clusters(pick_kernel(epi, xp, true), 2, smem_for(256, xp, true), sms, true);
+  const int pairs = active_pairs(pick_kernel(epi, xp, true), smem_for(256, xp, true), sms);
   if (pairs < 1) return TcChoice{};
   // tile height: a multiple of 32 (each CTA's half in TMA boxes of at least
   // 16 rows -- narrow boxes cost the producer more copies than the stage's
@@ -909,19 +858,18 @@ TcChoice choose(int epi, int xp, const GemmParams& g, int sms) {
   int cs = 1;
   if (forced > 0) {
     cs = forced;
-  } else if (share_mode() != 0) {
+  } else {
     if (xp == 1) cs = (R > 320 && R <= 512) ? 2 : 1;
     else if (R > 256 && R <= 512) cs = 2;
     else if (R > 512 && R <= 768) cs = 3;
     else if (R > 1024 && R <= 1536) cs = 6;
   }
   TcChoice c;
-  if (cs > 1 && cs <= kMaxCluster) {
+  if (cs > 1 && cs <= kMaxGroup) {
     c.nt = round_up((R + cs - 1) / cs, 16);
     c.n_tiles = (R + c.nt - 1) / c.nt;
     if (c.nt <= 256 && c.n_tiles == cs) {
-      const int groups =
-          active_clusters(pick_kernel(epi, xp, false), cs, smem_for(c.nt, xp), sms, share_mode() == 1);
+      const int groups = sms / cs;
       if (groups > 0) {
         const long long units = (long long)g.m_tiles * g.kb;
         c.cs = cs;
@@ -988,7 +936,6 @@ cudaError_t launch_gemm_tc(int epi, int xp, const CUtensorMap* a0, const CUtenso
   p.x_box = box_for(c.pair ? c.nt / 2 : c.nt);
   p.stages = tc_stages(c.nt, xp, c.pair);
   p.defer_fixup = (c.pair || c.cs > 1 || c.nt >= kDeferFixupRows) ? 1 : 0;
-  p.multicast = !c.pair && c.cs > 1 && share_mode() == 1 ? 1 : 0;
   const int smem = smem_for(c.nt, xp, c.pair);
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
@@ -1004,9 +951,9 @@ cudaError_t launch_gemm_tc(int epi, int xp, const CUtensorMap* a0, const CUtenso
     attr[na].val.programmaticStreamSerializationAllowed = 1;
     ++na;
   }
-  if (p.multicast || c.pair) {
+  if (c.pair) {
     attr[na].id = cudaLaunchAttributeClusterDimension;
-    attr[na].val.clusterDim.x = static_cast<unsigned>(c.pair ? 2 : c.cs);
+    attr[na].val.clusterDim.x = 2;
     attr[na].val.clusterDim.y = 1;
     attr[na].val.clusterDim.z = 1;
     ++na;

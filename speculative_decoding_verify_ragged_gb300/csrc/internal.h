@@ -77,7 +77,6 @@ struct GemmParams {
   // tg * cs + r of tile group tg), tile groups (n_tiles = n_groups * cs when
   // cs > 1), the activation map's box height and the pipeline depth
   int nt = 0, cs = 1, n_groups = 0, x_box = 0, stages = 0;
-  int multicast = 0;  // the cluster's CTAs share weight tiles by TMA multicast (else a group reads them via L2)
   // tcgen05 kernels: CTA pairs (cta_group::2) -- a unit is 256 weight rows,
   // 128 in each CTA, against the pair's nt activation rows, half loaded by each
   int pair = 0;
