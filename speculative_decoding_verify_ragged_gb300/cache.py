@@ -49,7 +49,8 @@ class PagedCache:
     cfg: n_q, n_kv, head_dim, page_size (16), cache_format ("bf16" or "e4m3"),
     rope_theta (0 or absent: append does not rotate).  The workspace is
     allocated here through torch, on the current device; calls of one
-    PagedCache must not overlap in time.
+    PagedCache must not overlap in time.  It may be let go while its calls are
+    still running, on whichever stream; a captured graph needs it as long as it is replayed.
     """
 
     def __init__(self, cfg: dict, max_rows: int, max_slots: int, lib_path: str | None = None):
@@ -64,6 +65,7 @@ class PagedCache:
         if nbytes == 0:
             raise SdvError(1, "sdv_cache_workspace_size rejected the configuration")
         self._setup(c, fmt, torch.empty(int(nbytes), dtype=torch.uint8, device="cuda"))
+        self._streams.add(torch._C._cuda_getCurrentRawStream(self._index))
         h = ctypes.c_void_p()
         self._check(self.lib.sdv_cache_create(ctypes.byref(self.cfg), _ptr(self.workspace), ctypes.c_size_t(nbytes),
                                               self.max_rows, self.max_slots, _stream(None), ctypes.byref(h)),
@@ -76,6 +78,7 @@ class PagedCache:
         self._index = workspace.get_device()
         self._n_q, self._n_kv, self._d = cfg.n_q, cfg.n_kv, cfg.head_dim
         self._geometry = (cfg.n_kv, cfg.head_dim, fmt, self._index)
+        self._streams = set()  # whose work the workspace's memory is known to wait for
 
     def close(self):
         if getattr(self, "handle", None):
@@ -186,6 +189,10 @@ class PagedCache:
         n_q, T = self._n_q, self._mine(chunk)
         qs, os_ = self._rows(q, "q", n_q, T, BF16), self._rows(out, "out", n_q, T, BF16)
         st, raw = self._enqueue(status, stream)
+        if raw not in self._streams:
+            # the allocator hands the workspace on only when this stream's work has ended
+            self.workspace.record_stream(torch.cuda.current_stream(self.device) if stream is None else stream)
+            self._streams.add(raw)
         rc = self.lib.sdv_cache_attention(self.handle, chunk.ref, q.data_ptr(), qs, out.data_ptr(), os_, st, raw)
         if rc:
             self._check(rc, "sdv_cache_attention")

@@ -30,6 +30,7 @@ def make_cache(n_q=4, n_kv=2, head_dim=64, fmt="bf16"):
     c = pc.PagedCache.__new__(pc.PagedCache)
     c.lib = Recorder()
     c._setup(SdvCacheConfig(n_q, n_kv, head_dim, 16, pc.FORMATS[fmt], 0.0), fmt, torch.empty(256, dtype=torch.uint8))
+    c._streams.add(STREAM.cuda_stream)
     c.handle = 1
     return c
 

@@ -40,3 +40,31 @@ def test_a_step_without_rows(fmt):
     assert s["status"].item() == 0 and torch.equal(s["pool"], pool)
     with pytest.raises(ValueError):
         c.read(chunk, None, None, s["status"])
+
+
+@pytest.mark.parametrize("how", ["argument", "current"])
+def test_a_workspace_let_go_while_another_stream_uses_it(how):
+    """The handle is dropped while its call waits on a side stream: its workspace's memory is not handed
+    to anyone before that call has ended."""
+    s = ch.make([2], [300], 8, 2, 128, "bf16", seed=3)
+    want, tol = ch.attention(s)
+    out = torch.zeros_like(s["q"])
+    c = _cache(s)
+    at, size = c.workspace.data_ptr(), c.workspace.numel()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(400_000_000)                  # a fifth of a second or so
+    chunk = _chunk(c, s)
+    if how == "argument":
+        c.attention(chunk, s["q"], out, s["status"], stream=side)
+    else:
+        with torch.cuda.stream(side):
+            c.attention(chunk, s["q"], out, s["status"])
+    del c
+    taken = [torch.empty(size, dtype=torch.uint8, device="cuda") for _ in range(3)]
+    waiting = not side.query()
+    assert waiting and at not in [t.data_ptr() for t in taken]
+    side.synchronize()
+    assert s["status"].item() == 0
+    assert ((out.double() - want).abs() <= tol).all()
