@@ -32,6 +32,11 @@ BF16, BOTH = (torch.bfloat16,), (torch.bfloat16, torch.float32)
 FORMATS = {"bf16": SDV_CACHE_BF16, "e4m3": SDV_CACHE_E4M3}
 
 
+def _c_int(x) -> int:
+    """x for a 32-bit field, which ctypes would wrap: the largest there is, or -1, beyond its ends."""
+    return max(-1, min(int(x), 2 ** 31 - 1))
+
+
 class Chunk:
     """A ragged chunk's description (sdv_chunk), the tensors that it points to and the geometry of their pages."""
 
@@ -58,9 +63,9 @@ class PagedCache:
         fmt = cfg.get("cache_format", "bf16")
         if fmt not in FORMATS:
             raise ValueError(f"cache_format {fmt!r}: one of {sorted(FORMATS)}")
-        c = SdvCacheConfig(int(cfg["n_q"]), int(cfg["n_kv"]), int(cfg["head_dim"]), int(cfg.get("page_size", 16)),
+        c = SdvCacheConfig(_c_int(cfg["n_q"]), _c_int(cfg["n_kv"]), _c_int(cfg["head_dim"]), _c_int(cfg.get("page_size", 16)),
                            FORMATS[fmt], float(cfg.get("rope_theta", 0.0)))
-        self.max_rows, self.max_slots = int(max_rows), int(max_slots)
+        self.max_rows, self.max_slots = _c_int(max_rows), _c_int(max_slots)
         nbytes = self.lib.sdv_cache_workspace_size(ctypes.byref(c), self.max_rows, self.max_slots)
         if nbytes == 0:
             raise SdvError(1, "sdv_cache_workspace_size rejected the configuration")
@@ -158,9 +163,9 @@ class PagedCache:
             self._want(kv_scales, "kv_scales", torch.uint8, pool_shape[:-1])
         elif kv_scales is not None:
             raise ValueError("kv_scales: a bf16 cache has none")
-        s = SdvChunk(B, int(rows), int(max_q), row_offsets.data_ptr(), kv_lens.data_ptr(), kv_pool.data_ptr(),
-                     kv_scales.data_ptr() if kv_scales is not None else None, int(kv_pool.shape[0]),
-                     page_table.data_ptr(), int(page_table.shape[1]), int(window))
+        s = SdvChunk(B, _c_int(rows), _c_int(max_q), row_offsets.data_ptr(), kv_lens.data_ptr(), kv_pool.data_ptr(),
+                     kv_scales.data_ptr() if kv_scales is not None else None, _c_int(kv_pool.shape[0]),
+                     page_table.data_ptr(), _c_int(page_table.shape[1]), _c_int(window))
         return Chunk(s, (row_offsets, kv_lens, page_table, kv_pool, kv_scales), self._geometry)
 
     # -- entry points ------------------------------------------------------

@@ -38,7 +38,7 @@ def make_cache(n_q=4, n_kv=2, head_dim=64, fmt="bf16"):
 def make_chunk(c, rows=3, pages=4, **kw):
     pool, scales = c.new_pool(pages)
     i32 = dict(dtype=torch.int32)
-    a = dict(rows=rows, max_q=rows, row_offsets=torch.tensor([0, rows], **i32), kv_lens=torch.tensor([rows], **i32),
+    a = dict(rows=rows, max_q=3, row_offsets=torch.tensor([0, 3], **i32), kv_lens=torch.tensor([3], **i32),
              page_table=torch.zeros((1, 2), **i32), kv_pool=pool, kv_scales=scales)
     a.update(kw)
     return c.chunk(**a)
@@ -76,3 +76,32 @@ def test_a_chunk_of_the_same_geometry_serves():
     for call in operators(twin, make_chunk(mine)):
         call()
     assert [n for n, _ in twin.lib.calls] == ["sdv_cache_append", "sdv_cache_attention", "sdv_cache_read"]
+
+
+def test_numbers_past_32_bits_keep_their_meaning():
+    """The C fields have 32 bits: a window or a bound longer than that stays one that covers all, a count is refused
+    by the library as too large, and a number below 0 stays below 0."""
+    c = make_cache()
+    top = 2 ** 31 - 1
+    s = make_chunk(c, window=2 ** 32 + 5, max_q=2 ** 32 + 1).struct
+    assert (s.window, s.max_q) == (top, top)
+    assert make_chunk(c, window=2 ** 31).struct.window == top
+    assert make_chunk(c, rows=2 ** 32 + 3).struct.T == top
+    s = make_chunk(c, window=-2 ** 32 + 5, max_q=-2 ** 31 - 1).struct
+    assert s.window < 0 and s.max_q < 0
+    # a handle: the library sees the sizes it is asked for, or larger ones than it takes
+    seen = []
+
+    class Sizes(Recorder):
+        def sdv_cache_workspace_size(self, cfg, rows, slots):
+            c = cfg._obj
+            seen.append((c.n_q, c.n_kv, c.head_dim, c.page_size, rows, slots))
+            return 0
+
+    real, pc.load_library = pc.load_library, lambda *a: Sizes()
+    try:
+        with pytest.raises(Exception, match="rejected"):
+            pc.PagedCache(dict(n_q=2 ** 32 + 4, n_kv=2 ** 32 + 2, head_dim=2 ** 32 + 64, page_size=2 ** 32 + 16), 2 ** 32 + 8, 2 ** 32 + 2)
+    finally:
+        pc.load_library = real
+    assert seen == [(top,) * 6]
