@@ -117,7 +117,7 @@ class PagedCache:
         n, st = t.shape, t.stride()
         if len(n) == 3 and t.dtype in dtypes and t.get_device() == self._index and n[0] >= rows and n[1] == heads \
                 and n[2] == d and st[2] == 1 and (st[1] == d or heads == 1):
-            return st[0] if n[0] > 1 else max(st[0], heads * d)
+            return st[0] if n[0] > 1 else heads * d
         if t.dtype not in dtypes:
             raise ValueError(f"{name}: {t.dtype}, one of {dtypes} is wanted")
         if t.get_device() != self._index:

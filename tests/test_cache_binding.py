@@ -105,3 +105,19 @@ def test_numbers_past_32_bits_keep_their_meaning():
     finally:
         pc.load_library = real
     assert seen == [(top,) * 6]
+
+
+def test_one_row_has_no_stride():
+    """The stride of a tensor of one row says nothing; the library, which wants 16 bytes of it, gets the row's width."""
+    c = make_cache(n_q=4, n_kv=2, head_dim=64)
+    chunk = make_chunk(c, rows=1)
+    row = lambda heads, st: torch.zeros(1024, dtype=torch.bfloat16).as_strided((1, heads, 64), (st, 64, 1))  # noqa: E731
+    st = torch.zeros(1, dtype=torch.int32)
+    for odd in (1, 3, 515):
+        c.attention(chunk, row(4, odd), row(4, odd), st, stream=STREAM)
+        c.append(chunk, row(2, odd), row(2, odd), st, q=row(4, odd), q_out=row(4, odd), stream=STREAM)
+        c.read(chunk, row(2, odd), row(2, odd), st, stream=STREAM)
+        (_, at), (_, ap), (_, rd) = c.lib.calls[-3:]
+        r = ap[2]._obj
+        assert (at[3], at[5]) == (256, 256) and (rd[3], rd[5]) == (128, 128)
+        assert (r.k_stride, r.v_stride, r.q_stride, r.q_out_stride) == (128, 128, 256, 256)
