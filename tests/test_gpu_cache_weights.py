@@ -23,8 +23,9 @@ pytestmark = pytest.mark.gpu
 N_Q, N_KV, D = 4, 2, 128
 
 
-def _sunk(q_len, kv, gap, size, seed):
-    """One sequence over codes: the sink at position 0, the other values size * (1 + randn / 4)."""
+def _sunk(q_len, kv, gap, size, seed, steps=0):
+    """One sequence over codes: the sink at position 0, the other values size * (1 + randn / 4).  With `steps`, every
+    that many keys stand `gap` times a number in [-1, 1] nats off the mean instead, and the values above it are 0."""
     s = ch.make([q_len], [kv], N_Q, N_KV, D, "e4m3", seed=seed, tail=0.0)
     g = torch.Generator(device="cuda").manual_seed(seed + 50)
     page, slot = s["table"][0].long()[torch.arange(kv, device="cuda") // 16], torch.arange(kv, device="cuda") % 16
@@ -34,6 +35,11 @@ def _sunk(q_len, kv, gap, size, seed):
     k[0, :, 0] = gap * math.sqrt(D) / 4.0
     v = size * (1.0 + 0.25 * torch.randn((kv, N_KV, D), generator=g, device="cuda"))
     v[0] = 0.0
+    if steps:
+        off = gap * (2.0 * torch.rand(-(-kv // steps), generator=g, device="cuda") - 1.0)
+        off = off.repeat_interleave(steps)[:kv]
+        k[:, :, 0] = (off * math.sqrt(D) / 4.0)[:, None]
+        v[off > 0] = 0.0
     exps = []
     for which, x in ((0, k), (1, v)):
         e = ch.exponent(x.abs().amax(-1))
@@ -78,9 +84,9 @@ def _bound(s, e, few):
     return out, tol
 
 
-def _check(rows, size, gap, copies, few):
+def _check(rows, size, gap, copies, few, steps=0):
     from speculative_decoding_verify_ragged_gb300.cache import PagedCache
-    s, e = _sunk(rows, 4096 + rows, gap, size, seed=rows + gap)
+    s, e = _sunk(rows, 4096 + rows, gap, size, seed=rows + gap, steps=steps)
     want, tol = _bound(s, e, few)
     c = PagedCache(dict(n_q=N_Q, n_kv=N_KV, head_dim=D, cache_format="e4m3"), max_rows=rows * copies, max_slots=copies)
     q = s["q"].repeat(copies, 1, 1)
@@ -110,3 +116,13 @@ def test_few_rows_beside_a_sink(rows, size, gap, copies):
 @pytest.mark.parametrize("gap", [10, 12, 14, 16, 18])
 def test_many_rows_beside_a_sink(rows, size, gap, copies):
     _check(rows, size, gap, copies, False)
+
+
+@pytest.mark.parametrize("copies", [1, 160])
+@pytest.mark.parametrize("rows", [1, 7, 9, 64])
+@pytest.mark.parametrize("gap", [3, 8, 15])
+def test_steps_up_and_down(rows, gap, copies):
+    """The bound follows pages (few rows) or steps of 64 keys that lie up to 30 nats apart, up and down in any
+    order; only those below the middle have values."""
+    few = rows * 2 <= 16
+    _check(rows, 0.1, gap, copies, few, steps=16 if few else 64)
