@@ -48,7 +48,9 @@ typedef struct {
 /* A ragged chunk of new tokens.
  *  B, T (host)      sequences, at least one; rows that the caller's row buffers hold.  With T = 0 a
  *                   call enqueues nothing and its row pointers may be null.
- *  max_q (host)     an upper bound of every sequence's rows.
+ *  max_q (host)     an upper bound of every sequence's rows.  It picks sdv_cache_attention's kernels (a
+ *                   captured call keeps them): one that is far too large costs time, a step of next tokens up to
+ *                   twice its own, and no result.
  *  row_offsets [B+1] (device) row_offsets[0] = 0, non-decreasing, row_offsets[B] <= T:
  *                   sequence b owns rows [row_offsets[b], row_offsets[b+1]).
  *                   Rows behind the last sequence's are not touched.

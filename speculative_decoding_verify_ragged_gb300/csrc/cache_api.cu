@@ -37,6 +37,23 @@ int sms_of(int dev) {
 // mma.sync kernel takes it: one of its 16-row items.
 constexpr int kSmallRows = 16;
 
+// Whether the sequences of few rows of a step that also brings longer ones go to
+// the mma.sync kernel, behind the tcgen05 kernel, or stay with it.  A second
+// launch costs 15 to 20 us; a next token costs the tcgen05 kernel an item's start and
+// end, and more per key the fewer bytes a key has.  So: where at least half of the sequences
+// must be short, and there are enough (sequence, key head)s for it.  One against
+// both kernels, 2 pieces of 300 rows and B - 2 next tokens over 600 to 6000 positions, 8 key heads unless said, us:
+//   keys of 256 bytes  B 32 105 : 126, 128 328 : 353; over 60 to 600, 2 heads, 256 65 : 68, 1000 198 : 137
+//   128 (codes)        B 16 81 : 85, 20 86 : 86, 24 111 : 101, 64 191 : 140; 4 heads, 40 75 : 84, 64 109 : 95; 1 head, 160 76 : 92, 320 131 : 111
+//   128 (bf16)         B 16 65 : 70, 20 65 : 65, 24 81 : 78, 64 150 : 120
+//   64                 B 8 62 : 65, 12 53 : 54, 20 67 : 57, 64 153 : 92; 2 heads, 40 37 : 48, 80 59 : 59
+// and by the share of pieces, codes of 128 bytes: 8 of 24 166 : 161, 31 of 64 557 : 527, 16 of 24 257 : 262.
+bool two_kernels(const sdv_cache* h, const sdv_chunk* c) {
+  const int key_bytes = h->cfg.head_dim * (h->cfg.cache_format == SDV_CACHE_E4M3 ? 1 : 2);
+  const int per_sm_x4 = key_bytes <= 64 ? 4 : key_bytes <= 128 ? 5 : 32;
+  return 4LL * c->B * h->cfg.n_kv >= (long long)per_sm_x4 * h->sms && c->T <= (long long)c->B * c->max_q / 2;
+}
+
 struct Space {
   size_t counters, counters_tc, cuts, part, part_tc, total;
 };
@@ -197,10 +214,7 @@ extern "C" sdv_status sdv_cache_attention(sdv_cache* h, const sdv_chunk* chunk, 
   const int group = h->cfg.n_q / h->cfg.n_kv;
   const long long rows = (long long)(chunk->max_q < chunk->T ? chunk->max_q : chunk->T) * group;  // of a sequence at most
   if (rows > kSmallRows) {
-    // The tcgen05 kernel takes every sequence, but where most must be far
-    // shorter than the longest (a step that mixes next tokens with pieces of
-    // prompts): there the mma.sync kernel takes those of few rows
-    const bool two = chunk->B >= 8 && chunk->T <= (long long)chunk->B * chunk->max_q / 2;
+    const bool two = two_kernels(h, chunk);
     p.small_rows = two ? kSmallRows : 0;
     p.part = h->part_tc;
     p.cuts = h->cuts;

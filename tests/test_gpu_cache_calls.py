@@ -68,3 +68,43 @@ def test_a_workspace_let_go_while_another_stream_uses_it(how):
     side.synchronize()
     assert s["status"].item() == 0
     assert ((out.double() - want).abs() <= tol).all()
+
+
+def _mixed(B, n_kv, d, fmt, pieces=2, seed=5):
+    g = torch.Generator().manual_seed(seed)
+    kv = torch.randint(1, 200, (B,), generator=g).tolist()
+    q = [1] * B
+    for i in range(pieces):                             # spread over the batch
+        at = i * (B - 1) // max(1, pieces - 1)
+        q[at], kv[at] = 40, 90 + i
+    return ch.make(q, kv, 4 * n_kv, n_kv, d, fmt, seed=seed)
+
+
+@pytest.mark.parametrize("fmt,d", [("bf16", 128), ("bf16", 64), ("e4m3", 128), ("e4m3", 64)])
+def test_a_mixed_step_takes_a_second_kernel_only_where_it_pays(fmt, d):
+    """Next tokens beside pieces of prompts: with few of them a second kernel's launch costs more than it saves, so
+    one takes all (it and the join, 2 launches); with many, both run (3).  The outputs are right either way."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    per_sm = {64: 1.0, 128: 1.25, 256: 8.0}[d * (2 if fmt == "bf16" else 1)]
+    edge = -(-int(per_sm * sms * 4) // 4)
+    for n_kv in (8, 2):
+        least = -(-edge // n_kv)
+        for B, launches in ((least - 1, 2), (least, 3), (8, 2)):
+            if B > 400:
+                continue
+            s = _mixed(B, n_kv, d, fmt)
+            want, tol = ch.attention(s)
+            c = _cache(s)
+            out = torch.full_like(s["q"], 7.0)
+            chunk = _chunk(c, s)
+            before = c.lib.sdv_kernel_launches()
+            c.attention(chunk, s["q"], out, s["status"])
+            assert c.lib.sdv_kernel_launches() - before == launches, (B, n_kv)
+            assert s["status"].item() == 0
+            assert ((out.double() - want).abs() <= tol).all(), (B, n_kv)
+    # half of the sequences pieces or more: one kernel
+    s = _mixed(64, 8, d, fmt, pieces=33)
+    c = _cache(s)
+    before = c.lib.sdv_kernel_launches()
+    c.attention(_chunk(c, s), s["q"], torch.empty_like(s["q"]), s["status"])
+    assert c.lib.sdv_kernel_launches() - before == 2 and s["status"].item() == 0
