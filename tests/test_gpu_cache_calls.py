@@ -71,10 +71,11 @@ def test_a_workspace_let_go_while_another_stream_uses_it(how):
 
 
 def _mixed(B, n_kv, d, fmt, pieces=2, seed=5):
+    """B - `pieces` next tokens and as many pieces of 40 rows, spread over the batch."""
     g = torch.Generator().manual_seed(seed)
     kv = torch.randint(1, 200, (B,), generator=g).tolist()
     q = [1] * B
-    for i in range(pieces):                             # spread over the batch
+    for i in range(pieces):
         at = i * (B - 1) // max(1, pieces - 1)
         q[at], kv[at] = 40, 90 + i
     return ch.make(q, kv, 4 * n_kv, n_kv, d, fmt, seed=seed)
@@ -108,3 +109,37 @@ def test_a_mixed_step_takes_a_second_kernel_only_where_it_pays(fmt, d):
     before = c.lib.sdv_kernel_launches()
     c.attention(_chunk(c, s), s["q"], torch.empty_like(s["q"]), s["status"])
     assert c.lib.sdv_kernel_launches() - before == 2 and s["status"].item() == 0
+
+
+@pytest.mark.parametrize("window", [0, 33])
+@pytest.mark.parametrize("fmt,d,n_q,n_kv", [("bf16", 64, 8, 4), ("e4m3", 64, 8, 4), ("e4m3", 128, 8, 4), ("bf16", 128, 16, 16)])
+def test_both_kernels_of_a_mixed_step(fmt, d, n_q, n_kv, window):
+    """Next tokens, sequences without rows, more rows than positions and pieces, each in both kernels' shares; then
+    the captured call over other lengths."""
+    B = 90
+    g = torch.Generator().manual_seed(7)
+    kv = torch.randint(1, 700, (B,), generator=g).tolist()
+    q = [1] * B
+    q[3], q[40], q[B - 1] = 300, 150, 40
+    q[5], q[6], q[7], kv[7], q[8], kv[8] = 0, 3, 2, 0, 30, 9
+    kv[3], kv[40], kv[B - 1] = 650, 150, 41
+    s = ch.make(q, kv, n_q, n_kv, d, fmt, seed=11, window=window)
+    c = _cache(s)
+    chunk, out = _chunk(c, s), torch.full_like(s["q"], 7.0)
+    before = c.lib.sdv_kernel_launches()
+    c.attention(chunk, s["q"], out, s["status"])
+    assert c.lib.sdv_kernel_launches() - before == 3 and s["status"].item() == 0
+    want, tol = ch.attention(s)
+    assert ((out.double() - want).abs() <= tol).all()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        c.attention(chunk, s["q"], out, s["status"])
+    for k in range(2):
+        lens = [max(0, n - 5 * k - b % 7) for b, n in enumerate(kv)]
+        s["lens"].copy_(torch.tensor(lens, dtype=torch.int32))
+        out.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        want, tol = ch.attention(dict(s, kv_lens=lens))
+        assert s["status"].item() == 0
+        assert ((out.double() - want).abs() <= tol).all()
