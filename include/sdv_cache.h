@@ -37,8 +37,8 @@ extern "C" {
  *   code * 2^e is exact in bf16 and in fp16. */
 enum { SDV_CACHE_BF16 = 0, SDV_CACHE_E4M3 = 1 };
 
-/* n_q a multiple of n_kv; head_dim 64 or 128; page_size 16; rope_theta >= 0: the
- * rotary base of sdv_cache_append (0: keys and queries are not rotated). */
+/* n_q <= 65536, a multiple of n_kv; head_dim 64 or 128; page_size 16; rope_theta 0 or >= 1:
+ * the rotary base of sdv_cache_append (0: keys and queries are not rotated). */
 typedef struct {
   int n_q, n_kv, head_dim, page_size;
   int cache_format;
@@ -78,8 +78,8 @@ typedef struct {
 typedef struct sdv_cache sdv_cache;
 
 /* Bytes of device workspace (partial results of key ranges cut between thread
- * blocks, and their counters) for chunks of up to max_rows rows and max_slots
- * (<= 1024) sequences.  0 on an invalid configuration. */
+ * blocks, and their counters) for chunks of up to max_rows rows (max_rows * n_q
+ * below 2^30) and max_slots (<= 1024) sequences.  0 on an invalid configuration. */
 size_t sdv_cache_workspace_size(const sdv_cache_config *cfg, int max_rows, int max_slots);
 
 /* Create a handle on the current device.  `workspace` (device, caller-owned, >=

@@ -77,7 +77,8 @@ __device__ __forceinline__ int2 row_place(const ChunkParams& c, const int* s_off
 // as integers before the rest is rounded to fp32.
 //
 // Bound by the input's bytes.  8192 rows of 48 heads of 128, fp32 to e4m3 and
-// queries to bf16 (285 MB): 48.4 us, 5.9 TB/s.
+// queries to bf16 (285 MB): 48.1 us, 5.9 TB/s.  3635 rows of 16 heads, bf16 (30 MB): 9.6 us, 3.1 TB/s: 909 blocks of
+// one round each, of which 456 are resident, so two waves of waits, checks and loads.
 template <int D, int FMT, typename T>
 __global__ void __launch_bounds__(IO_THREADS)
     cache_append_kernel(const AppendParams p, const __grid_constant__ RopeTurns turns, int per) {
@@ -189,7 +190,8 @@ __global__ void __launch_bounds__(IO_THREADS)
 
 // A warp takes a row (of few rows several take one), a lane 16 bytes of codes or
 // 16-bit values of one of its heads, eight at a time; the next row's place is found meanwhile.  Bound by
-// the bytes: 32749 positions of 8 heads of 128, bf16 (268 MB), 42.6 us, 6.3 TB/s.
+// the bytes: 32749 positions of 8 heads of 128, bf16 (268 MB), 42.8 us, 6.3 TB/s; e4m3 to bf16 (202 MB) 41.9 us,
+// 4.8 TB/s; to fp32, bf16 (402 MB) 77.3 us, 5.2 TB/s, e4m3 (336 MB) 84.6 us, 4.0 TB/s.
 template <int D, int FMT, int OUT>
 __global__ void __launch_bounds__(IO_THREADS) cache_read_kernel(const ReadParams p, int split) {
   extern __shared__ int s_meta[];

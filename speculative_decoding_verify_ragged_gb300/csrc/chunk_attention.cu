@@ -19,9 +19,9 @@
 //
 // Bound by the cache's bytes where there are enough of them (32 query and 8 key
 // heads of 128): 64 sequences of 1000 to 9000 tokens, one row each, bf16 1.33 GB
-// in 208 us (0.94 of the copy peak), e4m3 670 MB in 121 us (0.81; the conversions and
+// in 208 us (0.94 of the copy peak), e4m3 670 MB in 122 us (0.81; the conversions and
 // three blocks per SM hold it there); 128 sequences of 2048 tokens, 4 rows each, bf16
-// 181 us (0.88).  Small batches are a chain of latencies: 1 sequence of 517
+// 182 us (0.88), e4m3 158 us (0.52: 237 registers leave two blocks per SM, a page on its way each warp).  Small batches are a chain of latencies: 1 sequence of 517
 // tokens 9.1 us, of which the kernel's own 4.8.
 #include "chunk.cuh"
 
@@ -117,6 +117,8 @@ struct Plan {
 // Blocks per SM: what the registers allow (held: two pages, the output, the
 // queries).  e4m3, 8 rows: 2, 3 and 4 blocks 149, 122 and 125 us for 64 sequences;
 // bf16, 8 rows: 2 and 3 blocks 209 and 228 us; 16 rows: 1 and 2 blocks 270 and 181 us.
+// Heads of 64, bf16, 8 rows: 3, 4 and 5 blocks 124, 118 and 140 us; 16 rows: 2, 3 and 4 135, 110 and 123; e4m3, 8 rows:
+// 87, 73 and 67; 16 rows: 172, 123 and 110 (one more of each would serve it; 5 want a larger workspace).
 template <int D, int FMT, int NT>
 constexpr int per_sm() {
   return D == 64 ? (NT == 1 ? 4 : 3) : FMT == SDV_CACHE_E4M3 ? (NT == 1 ? 3 : 2) : 2;
@@ -214,7 +216,7 @@ __global__ void __launch_bounds__(CA_THREADS, per_sm<D, FMT, NT>()) chunk_attn_k
   }
 
   for (long long u = blockIdx.x * s_plan.run;;) {
-    // (the plan is read anew for each item: held across the pages it would spill)
+    // (the plan is read anew for each item: held across the pages it spilled; the bf16 kernel of 16 rows still spills 36 bytes)
     const bool pieces = s_plan.pieces;
     const long long units = s_base[B], per_cta = s_plan.per, run = s_plan.run, u_end = min(units, (blockIdx.x + 1) * run);
     if (u >= u_end) break;

@@ -24,14 +24,14 @@
 // shared memory, so that nothing behind a sequence's end is ever multiplied.
 //
 // What bounds it, 32 query and 8 key heads of 128, bf16: 2048 new tokens over 32749
-// take 665 us in a graph's replays (1600 TFLOP/s, 0.84 of the burst peak, 0.94 of the sustained one; back
-// to back for long the power limit holds it at 732 us).  A block of two tiles takes 2780 cycles: its
+// take 725 to 750 us back to back (1450 TFLOP/s, 0.76 of the burst peak, 0.85 of the sustained one: the power
+// limit holds it there; a few calls after a pause take 667).  A block of two tiles takes 2780 cycles: its
 // products 2560 (N = 64 scores wait for shared memory: 48 cycles each in place
 // of 32, measured), the rest is the round from a step's weights to the scores
 // after next.  Scores of 128 keys at once into one buffer, their weights in
 // halves, the tiles taking turns, were slower (903 us: the softmax waits for each round).  One
 // issuing thread for both tiles under `lane == 0` issued at 70 cycles a product (1001 us).
-// With codes the same work takes 752 us, and 64 sequences of 16 rows 246 us against
+// With codes the same work takes 758 us, and 64 sequences of 16 rows 248 us against
 // 229 in bf16: a step of two tiles takes 1600 cycles in place of 1390, for the four
 // converting warps share the issue slots and the instruction cache with the softmax (without its
 // exponentials a step takes as long).  What helped is less code and fewer instructions:
@@ -65,7 +65,10 @@ constexpr float kMost = 16384.f, kMostCodes = 60000.f;
 // range and need none of it.  (kAbove 2, 4, 6, 8: six pieces of prompts 95.4, 94.4, 94.4, 96.4 us, 91.2 without
 // moves down; 2048 tokens over 8200 195.0, 195.0, 195.4, 199.4 us, 194.5 without.)
 constexpr float kAbove = 4.f, kLeast = 0x1p-8f, kSumMost = 0x1p50f, kDropMost = 48.f;
-constexpr int kJoinHere = 4;         // an item of up to this many parts more than one is joined by its last block
+// An item of up to this many parts more than one is joined by its last block, one of more by chunk_join_kernel
+// (2, 4, 6: 64 sequences x 8 rows over codes, heads of 64, 165, 171, 186 us, of 128 235, 236, 237; 4096 new
+// tokens, bf16, heads of 128, 119, 120, 121).
+constexpr int kJoinHere = 4;
 
 constexpr int MMA_WARP = 8, TMA_WARP = 10, CONV_WARP = 12;  // MMA_WARP + t issues tile t's products, TMA_WARP + 1 copies V
 
@@ -255,9 +258,11 @@ __device__ __forceinline__ Tile make_tile(const SeqRows& s, const Item& it, int 
 
 // What a block of the item costs, and an item before its first block (query,
 // first scores, output), in eighths of a block of two tiles: a block
-// of one tile takes 2450 cycles against 2750; items at 3 blocks were the fastest of
-// 3 to 5.5 (six prompts 82 us, 84 at 4.5).
-// (With every block alike the SMs with the short items ended last: 4096 new tokens 193 us, now 120.)
+// of one tile takes 2450 cycles against 2750 (bf16, heads of 128; measured there and used for all).
+// Items at 1.5, 3 and 4.5 blocks, us: 4096 new tokens bf16 134, 120, 122, heads of 64 104, 99, 101, codes 159, 139, 138;
+// six pieces of prompts bf16 106, 103, 103, codes 120, 119, 115.  Blocks of one tile at 8 in place of 7: within 2 %
+// either way, but six pieces over codes 119 -> 115.
+// (With items free the SMs with the short ones ended last: 4096 new tokens 193 us.)
 __device__ __forceinline__ int weight(const Item& it) { return it.rows > BM ? 8 : 7; }
 constexpr int kItemCost = 24;
 __device__ __forceinline__ int units_of(const Item& it) { return kItemCost + it.blocks * weight(it); }
@@ -366,7 +371,7 @@ __global__ void __launch_bounds__(Cfg<D, FMT>::THREADS, 1)
   }
   long long u_begin = 0, u_end = 0, per_cta = 1;
   if (good) {
-    // units (blocks times tiles) of one key head of each sequence, a warp a sequence, into the ring (not in use yet)
+    // units (items and blocks by what they cost) of one key head of each sequence, a warp a sequence, into the ring (not in use yet)
     long long* s_units = reinterpret_cast<long long*>(smem);  // [B]
     for (int b = warp; b < B; b += blockDim.x / kWarp) {
       const SeqRows s = seq_of(b);
