@@ -119,7 +119,7 @@ sdv_status sdv_cache_append(sdv_cache *cache, const sdv_chunk *chunk, const sdv_
  * elements (16-byte aligned, strides multiples of 8).  Scores, the softmax's maximum and
  * sum and the output are held in 32 bits; the weights enter the second product
  * in 16 bits (bf16 over a bf16 cache; fp16 over codes, where a small weight is rounded to a multiple of at most
- * 2^-16 of what it and the 63 keys beside it add up to).  Positions behind a sequence's end are never used, whatever they hold; the cached
+ * 2^-15 of what the keys beside it add up to).  Positions behind a sequence's end are never used, whatever they hold; the cached
  * values that the chunk's rows see are taken to be finite. */
 sdv_status sdv_cache_attention(sdv_cache *cache, const sdv_chunk *chunk, const void *q, long long q_stride, void *out,
                                long long out_stride, int *status, void *stream);

@@ -50,6 +50,7 @@ constexpr int kSmallRows = 16;
 // and by the share of pieces, codes of 128 bytes: 8 of 24 166 : 161, 31 of 64 557 : 527, 16 of 24 257 : 262.
 bool two_kernels(const sdv_cache* h, const sdv_chunk* c) {
   const int key_bytes = h->cfg.head_dim * (h->cfg.cache_format == SDV_CACHE_E4M3 ? 1 : 2);
+  if (h->cfg.n_q / h->cfg.n_kv > kSmallRows) return false;  // a single token has too many rows for it
   const int per_sm_x4 = key_bytes <= 64 ? 4 : key_bytes <= 128 ? 5 : 32;
   return 4LL * c->B * h->cfg.n_kv >= (long long)per_sm_x4 * h->sms && c->T <= (long long)c->B * c->max_q / 2;
 }

@@ -143,3 +143,15 @@ def test_both_kernels_of_a_mixed_step(fmt, d, n_q, n_kv, window):
         want, tol = ch.attention(dict(s, kv_lens=lens))
         assert s["status"].item() == 0
         assert ((out.double() - want).abs() <= tol).all()
+
+
+def test_no_second_kernel_for_groups_past_its_rows():
+    """A single token of a group of 17 is past the 16 packed rows of the few-row kernel: it is not launched for nothing."""
+    s = ch.make([30, 30] + [1] * 158, [40, 60] + list(range(1, 159)), 34, 2, 64, "e4m3", seed=2)
+    c = _cache(s)
+    out = torch.full_like(s["q"], 7.0)
+    before = c.lib.sdv_kernel_launches()
+    c.attention(_chunk(c, s), s["q"], out, s["status"])
+    assert c.lib.sdv_kernel_launches() - before == 2 and s["status"].item() == 0
+    want, tol = ch.attention(s)
+    assert ((out.double() - want).abs() <= tol).all()
