@@ -326,7 +326,7 @@ def _plan_plain(s, new_rows, lens):
     there = b < B
     b = b.clamp(max=B - 1)
     pos = lens[b] - ends[b] + row
-    page = table.reshape(-1)[b * W + pos.clamp(0, W * PAGE - 1) // PAGE].long()   # (of rows behind the last: any)
+    page = table.reshape(-1)[b * W + pos.clamp(min=0) // PAGE].long()
     s["row_request"].copy_(torch.where(there, b, -1))
     s["positions"].copy_(torch.where(there, pos, -1))
     s["slots"].copy_(torch.where(there & (pos >= 0), page * PAGE + pos % PAGE, -1))
