@@ -34,7 +34,9 @@ extern "C" {
  *                   0, 0).  temperature 0 takes the largest logit (the first of equals); else
  *                   1e-30 .. 1e30.  top_k 0: off.  top_p in (0, 1], 1: off.  min_p in [0, 1], 0: off.
  *  uniforms [rows]  fp32 in [0, 1); may be NULL when tokens is.
- *  tokens [rows] int or NULL, probs fp32 [rows, probs_stride] or NULL, not both.
+ *  tokens [rows] int or NULL, probs fp32 [rows, probs_stride] or NULL, not both NULL.  They overlap
+ *                   no input.  probs and logits that do are refused (SDV_ERR_INVALID_ARG): their address
+ *                   ranges are apart, or they are columns of rows equally far apart in bytes.
  *
  * In order (logit descending, index ascending): the first top_k stay; of those
  * the shortest run whose sum of w = exp((z - max) / temperature) reaches top_p times theirs;

@@ -43,6 +43,7 @@
 #include "../../include/sdv_sample.h"
 #include "common.cuh"
 #include "internal.h"
+#include "rows.h"
 
 namespace cg = cooperative_groups;
 
@@ -1274,6 +1275,9 @@ extern "C" sdv_status sdv_sample(const sdv_sample_rows* r, int* status, void* st
   if (!r->tokens && !r->probs) return SDV_ERR_INVALID_ARG;
   if (r->tokens && !r->uniforms) return SDV_ERR_INVALID_ARG;
   if (r->probs && (r->probs_stride < r->vocab || (reinterpret_cast<uintptr_t>(r->probs) & 3))) return SDV_ERR_INVALID_ARG;
+  // (zeros are written while the row is read, and a row may be read again)
+  if (r->probs && rows_share(r->logits, r->stride * bytes, 1LL * r->vocab * bytes, r->probs, r->probs_stride * 4, 4LL * r->vocab, r->rows))
+    return SDV_ERR_INVALID_ARG;
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);

@@ -28,9 +28,10 @@ def sample(logits, status, *, uniforms=None, tokens=None, probs=None, temperatur
     """Filter each row of logits [rows, vocab] (bf16 or fp32, rows strided) under its request's settings.
 
     tokens [rows] int32 gets a token drawn with uniforms [rows] fp32, probs [rows, vocab] fp32 (rows strided) the
-    distribution that it is drawn from; one of them or both.  temperature, top_p, min_p fp32 and top_k int32 [requests]
-    are device tensors, None for 1, 1, 0 and 0 (off); row_request [rows] int32 says which request's a row takes (None:
-    row r is request r; negative: the row's outputs are left as they are).  lib: a load_library() other than libsdv.so.
+    distribution that it is drawn from; one of them or both, in memory of their own (probs over logits is refused).
+    temperature, top_p, min_p fp32 and top_k int32 [requests] are device tensors, None for 1, 1, 0 and 0 (off);
+    row_request [rows] int32 says which request's a row takes (None: row r is request r; negative: the row's outputs are
+    left as they are).  lib: a load_library() other than libsdv.so.
     """
     index = logits.get_device()
     dtype = logits.dtype
