@@ -1194,11 +1194,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
       kept.inv = t_from > 0.f ? __fdiv_ru(Kept::SPAN, t_from) : 0.f;
       float others = 0.f;
       if (sums) others = warp_sum(lane < blocks && theirs->block_rest > 0.f ? theirs->block_rest * exp2f((theirs->block_ref - top) * c) : 0.f);
-      // in steps of 2^-42.  Its error, up to t = 32: 1.25 * 2^-23 of t, so 2^-18 of a term and as much of the scale to `top`, 2^-22 of
-      // each exponential, 2^-16 of a thread's sums of up to 250 terms: below 2^-15 together.  Beyond t = 32 2^20 tokens add up to
-      // 2^-12 of the largest weight at most, with errors of 2^-16: 2^-28.
+      // in steps of 2^-42.  Its error, up to t = 32: of t a difference, a product, the quotient log2(e) / T (2^-24 each) and log2(e) itself
+      // (2^-26), alike for the scale to `top`, 1.7 * 2^-23 of t in all, so 2^-17.7 of a term; 2^-22 of each exponential; 2^-16 of a
+      // thread's sums of up to 250 terms: below 2^-15 together.  Beyond t = 32 2^20 tokens add up to 2^-12 of the largest weight at
+      // most, with errors of 2^-16: 2^-28.  What the sum stands for has each token rounded to a step, half of one away at most.
       const u64 sum = static_cast<u64>(others * 4398046511104.f);
-      told = answer(kept, g, whole, sum, sums ? (sum >> 15) + (1 << 14) : 0, a);
+      const u64 off = (sum >> 15) + (1 << 14) + p.r.vocab / 2;
+      told = answer(kept, g, whole, sum, sums ? off : 0, a);
     }
     if (!told) {
       cluster.sync();  // findings and sums have been read
