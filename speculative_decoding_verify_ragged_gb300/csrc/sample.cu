@@ -145,37 +145,38 @@ __device__ __forceinline__ u32 order_of(float z) {
 }
 __device__ __forceinline__ float value_of(u32 o) { return __uint_as_float(o ^ ((o >> 31) ? 0x80000000u : 0xFFFFFFFFu)); }
 
-// A row's weights.
+// A row's weights.  What decides which weight, level or bin a token has is written in steps that round by themselves (no product is taken
+// into the sum after it): lost() is what those roundings took off, and every pass has to give a token the same number.
 struct Weights {
   float top, c, c_low;  // maximum, log2(e) / T in two parts
   const PowerTable* powers;
 
-  __device__ __forceinline__ float t_of(float z) const { return z == top ? 0.f : (top - z) * c; }
+  __device__ __forceinline__ float t_of(float z) const { return z == top ? 0.f : __fmul_rn(__fsub_rn(top, z), c); }
   // what the three roundings on the way to t took off
   __device__ __forceinline__ float lost(float z, float t) const {
-    const float d = top - z;
+    const float d = __fsub_rn(top, z);
     const bool swap = fabsf(z) > fabsf(top);
     const float big = swap ? -z : top, small = swap ? top : -z;
-    const float rest = small - (d - big);
+    const float rest = __fsub_rn(small, __fsub_rn(d, big));
     return fmaf(rest, c, fmaf(d, c_low, fmaf(d, c, -t)));
   }
   __device__ __forceinline__ u64 fine(float z, float t) const {
-    const float shifted = t + 12288.f;  // floats about 12288 come in steps of 2^-10
+    const float shifted = __fadd_rn(t, 12288.f);  // floats about 12288 come in steps of 2^-10
     const int i = __float_as_int(shifted) - __float_as_int(12288.f);
-    const float x = (t - (shifted - 12288.f)) + lost(z, t);  // within 2^-11
+    const float x = __fadd_rn(__fsub_rn(t, __fsub_rn(shifted, 12288.f)), lost(z, t));  // within 2^-11
     const int j = i & (kSteps - 1);
     // 2^-x - 1 = -x ln 2 + (x ln 2)^2 / 2 - ..., the next term below 2^-37
-    const float q = x * fmaf(x, 0.2402265069591007f, -kLn2);
+    const float q = __fmul_rn(x, fmaf(x, 0.2402265069591007f, -kLn2));
     const int n = i >> 10;
-    const u64 v = powers->fixed[j] + static_cast<long long>(__float2int_rn(powers->value[j] * (q * 4398046511104.f)));
+    const u64 v = powers->fixed[j] + static_cast<long long>(__float2int_rn(__fmul_rn(powers->value[j], __fmul_rn(q, 4398046511104.f))));
     return n == 0 ? v : (v + (1ull << (n - 1))) >> n;
   }
   // 2^-t in fp32.  Of what t lost, all but the difference's rounding is put right: that is t 2^-25 at most
   __device__ __forceinline__ float rough(float z, float t, float scale) const {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(-t));
-    const float d = top - z;
-    return y * fmaf(fmaf(d, c_low, fmaf(d, c, -t)), -kLn2 * scale, scale);
+    const float d = __fsub_rn(top, z);
+    return __fmul_rn(y, fmaf(fmaf(d, c_low, fmaf(d, c, -t)), -kLn2 * scale, scale));
   }
   // t from 13 on, below 2^29
   __device__ __forceinline__ u32 coarse(float z, float t) const { return __float2uint_rn(rough(z, t, 4398046511104.f)); }
@@ -379,7 +380,7 @@ struct Row {
 
   // t in levels.  Of 32 the last 16 are four times as wide: a bound falls near the largest weights or far off.
   __device__ __forceinline__ float scaled(float t) const {
-    const float x = t * inv;
+    const float x = __fmul_rn(t, inv);
     return Source::LONG || x < 16.f ? x : fmaf(x, 0.25f, 12.f);
   }
   // 0 .. LEVELS - 1, LEVELS beyond the last level (-inf too)
@@ -753,7 +754,7 @@ struct Row {
     u32 count = level < LEVELS ? s.all_count[level] - base_count : kList + 1;
     int bin = -1;                        // once the histogram by t has named it
     u32 low = 0, high = 0xFFFFFFFFu;     // the candidates' order, once narrowed
-    auto bin_of = [&](float t) { return min(max(static_cast<int>((scaled(t) - level) * kBins), 0), kBins - 1); };
+    auto bin_of = [&](float t) { return min(max(static_cast<int>(__fmul_rn(__fsub_rn(scaled(t), static_cast<float>(level)), static_cast<float>(kBins))), 0), kBins - 1); };
     auto candidate = [&](float z) {
       const float t = w.t_of(z);
       if (level_at(t) != level || !(z > -INFINITY) || (bin >= 0 && bin_of(t) != bin)) return false;

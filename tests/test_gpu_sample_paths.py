@@ -175,6 +175,32 @@ def test_what_lies_below_half_a_step_adds_nothing(rows, steps_off):
     assert tokens.tolist() == [0 if steps_off > 0 else 1] * rows
 
 
+@pytest.mark.parametrize("top,temperature", [(0.0, 1.0), (0.1, 1.0), (3.7, 0.7), (-11.3, 3.3)])
+def test_weights_are_good_to_two_to_the_minus_34(top, temperature):
+    """128 equal largest tokens and 64872 of one other weight w: under top-p of p stay ceil(p (128 + 64872 w)) of the largest.  p is taken
+    next to where that changes, as near as fp32 comes (2^-24 of it); w is within 2^-34 and half a step of 2^-42, 2^-32.4 of itself
+    together (t is 10 at most), so bounds nearer than 2^-31 are left out."""
+    first, n = 128, 65000
+    rng = np.random.default_rng(5)
+    top, c = float(np.float32(top)), float(np.float32(temperature))
+    for t in rng.uniform(8.05, 9.95, 6):
+        low = float(np.float32(top - t * np.log(2.0) * c))
+        w = np.exp((low - top) / c)
+        total = first + (n - first) * w
+        ps, want = [], []
+        for m in range(1, first):
+            p = np.float32(m / total)
+            for q in (np.nextafter(p, np.float32(0)), p, np.nextafter(p, np.float32(1))):
+                if abs(float(q) * total / m - 1.0) > 2.0 ** -31:
+                    ps.append(float(q))
+                    want.append(int(np.ceil(float(q) * total)))
+        rows = len(ps)
+        z = torch.full((rows, n), low, device="cuda")
+        z[:, 7:7 + 500 * first:500] = top
+        _, probs = _run(z, torch.zeros(rows, device="cuda"), _settings(rows, temperature=temperature, top_p=ps))
+        assert (probs > 0).sum(1).tolist() == want, t
+
+
 def test_random_rows_and_settings():
     """Unlike lengths, kinds of rows and settings in one call each."""
     rng = np.random.default_rng(8)
