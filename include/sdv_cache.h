@@ -144,6 +144,9 @@ sdv_status sdv_cache_read(sdv_cache *cache, const sdv_chunk *chunk, void *k_out,
  *                   row_offsets[b+1]), the i-th of n at position lens[b] - n + i; slots: page * 16 +
  *                   position % 16, -1 for an empty row; last_rows: the request's last row, -1 for
  *                   none.  Entries of row_request, positions and slots behind the last row are -1.
+ *  max_B (host)     0, or the requests that row_offsets [max_B+1] and last_rows [max_B] have room for, B .. 1024: those
+ *                   behind the B have no rows in this step (their offsets are the last one, their last
+ *                   rows -1), so that a chunk of max_B sequences serves steps of any B.
  * row_offsets, lens, page_table are what a chunk (above) takes, row_request and
  * row_offsets what sampling (sdv_sample.h) and adapters (sdv_adapter.h) take. */
 typedef struct {
@@ -157,6 +160,7 @@ typedef struct {
   int *num_free;
   int *row_offsets, *row_request, *positions, *last_rows;
   long long *slots;
+  int max_B;
 } sdv_cache_tables;
 
 /* Give every request the ceil(lens[b] / 16) pages that its length needs and describe the step's rows.

@@ -116,7 +116,7 @@ class SdvCacheTables(ctypes.Structure):
     _fields_ = [("B", c_int), ("T", c_int), ("new_rows", c_void_p), ("lens", c_void_p), ("page_table", c_void_p),
                 ("max_pages_per_seq", c_int), ("page_counts", c_void_p), ("free_pages", c_void_p),
                 ("num_pool_pages", c_int), ("num_free", c_void_p), ("row_offsets", c_void_p), ("row_request", c_void_p),
-                ("positions", c_void_p), ("last_rows", c_void_p), ("slots", c_void_p)]
+                ("positions", c_void_p), ("last_rows", c_void_p), ("slots", c_void_p), ("max_B", c_int)]
 
 
 class SdvSampleRows(ctypes.Structure):

@@ -227,7 +227,8 @@ class Tables:
     Tensors, all int32 on the current device but slots (int64): page_table [max_slots, max_pages_per_seq], page_counts
     [max_slots], free_pages [num_pages] and num_free [1] are the state, at first every page free; row_offsets
     [max_slots + 1], row_request, positions, slots [max_rows] and last_rows [max_slots] describe the step that was
-    planned last.  They keep their addresses, so that a chunk made of them serves every step, captured ones too.
+    planned last.  They keep their addresses, so that a chunk made of them serves every step, captured ones too; in a step
+    of fewer requests than max_slots the others have no rows (last_rows -1).
     """
 
     def __init__(self, max_slots: int, max_rows: int, max_pages_per_seq: int, num_pages: int, lib_path: str | None = None):
@@ -255,7 +256,7 @@ class Tables:
         s = SdvCacheTables(B, self.max_rows, None, None, self.page_table.data_ptr(), self.max_pages_per_seq,
                            self.page_counts.data_ptr(), self.free_pages.data_ptr(), self.num_pages, self.num_free.data_ptr(),
                            self.row_offsets.data_ptr(), self.row_request.data_ptr(), self.positions.data_ptr(),
-                           self.last_rows.data_ptr(), self.slots.data_ptr())
+                           self.last_rows.data_ptr(), self.slots.data_ptr(), self.max_slots)
         self._structs[B] = s, ctypes.byref(s)
         return self._structs[B]
 

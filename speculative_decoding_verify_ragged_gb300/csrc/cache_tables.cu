@@ -116,6 +116,10 @@ __global__ void __launch_bounds__(TAB_THREADS) cache_plan_kernel(const sdv_cache
       p.row_offsets[t] = s_off[t];
       if (p.last_rows) p.last_rows[t] = n > 0 ? s_off[t] + n - 1 : -1;
     }
+    if (rank == 0 && t >= p.B && t < p.max_B) {
+      p.row_offsets[t + 1] = s_off[p.B];
+      if (p.last_rows) p.last_rows[t] = -1;
+    }
     if (rank == 0 && t == 0) {
       p.row_offsets[p.B] = s_off[p.B];
       *p.num_free = static_cast<int>(have - tot[2]);
@@ -174,7 +178,8 @@ extern "C" sdv_status sdv_cache_plan(const sdv_cache_tables* p, int* status, voi
     return SDV_ERR_INVALID_ARG;
   if (!p->new_rows || !p->lens || !p->page_table || !p->page_counts || !p->free_pages || !p->num_free || !p->row_offsets)
     return SDV_ERR_INVALID_ARG;
-  if (p->B > kMaxChunkSlots) return SDV_ERR_CAPACITY;
+  if (p->max_B < 0 || (p->max_B > 0 && p->max_B < p->B)) return SDV_ERR_INVALID_ARG;
+  if (p->B > kMaxChunkSlots || p->max_B > kMaxChunkSlots) return SDV_ERR_CAPACITY;
   const cudaError_t e = launch_cache_plan(*p, status, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? SDV_OK : cuda_fail(e);
 }
