@@ -46,7 +46,8 @@ void sdv_adapters_destroy(sdv_adapters *adapters);
  *  base, out [T, n]    y_format 0 = bf16, 1 = fp32; out may be base, else it overlaps neither base nor x.
  * Pointers 16-byte aligned, strides multiples of 16 bytes.
  * out = base + scale * (x A^T) B^T: products of the values as they are (fp32 x as a sum of three bf16, the rank values of three for an
- * fp32 out and two for a bf16 one), sums in fp32, rounded once to out's format. */
+ * fp32 out and two for a bf16 one), sums in fp32, rounded once to out's format.  Infinities and NaN do what fp32 arithmetic does with
+ * them (0 * inf and inf - inf are NaN), in their own rows only; finite values take part whatever their size. */
 typedef struct {
   int B, T;
   const int *row_offsets, *adapter_ids;

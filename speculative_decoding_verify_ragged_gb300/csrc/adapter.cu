@@ -108,12 +108,14 @@ __device__ __forceinline__ int item_request(const int* first, int B, int i) {
   return lo;
 }
 
-// x as the sum of P bf16 (within 2^-9P of it), pairs packed.
+// x as the sum of P bf16 (within 2^-9P of it), pairs packed.  All but the last stop at bf16's largest value: what lies between it and
+// fp32's keeps its rest, and an infinity stays one in the sum (an infinite first part would leave inf - inf to the others).
 template <int P>
 __device__ __forceinline__ void split(float x0, float x1, uint32_t (&w)[P]) {
 #pragma unroll
   for (int i = 0; i < P; ++i) {
-    w[i] = pack_bf16x2(x0, x1);
+    if (i < P - 1) asm("cvt.rn.satfinite.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(x1), "f"(x0));
+    else w[i] = pack_bf16x2(x0, x1);
     x0 -= __uint_as_float(w[i] << 16);
     x1 -= __uint_as_float(w[i] & 0xFFFF0000u);
   }
@@ -349,7 +351,8 @@ __global__ void __launch_bounds__(AD_THREADS, 2) adapter_kernel(const AdapterPar
       }
       wait_copies<0>();
       __syncthreads();  // the slabs have been read
-      // the shares' parts, [share][row][R], then their sum in place of the first
+      // the shares' parts, [share][row][R], then their sum in place of the first.  Ranks behind the adapter's are 0 whatever x is (an
+      // infinity times their zeros is not)
       const int stride = tiles * 8 * R;
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
@@ -359,7 +362,7 @@ __global__ void __launch_bounds__(AD_THREADS, 2) adapter_kernel(const AdapterPar
         for (int m = 0; m < MT; ++m)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            part[share * stride + (tile * 8 + q * 2 + (e & 1)) * R + m * 16 + g + (e >> 1) * 8] = acc[t][m][e];
+            part[share * stride + (tile * 8 + q * 2 + (e & 1)) * R + m * 16 + g + (e >> 1) * 8] = m * 16 + (e >> 1) * 8 < p.rank ? acc[t][m][e] : 0.f;
       }
       __syncthreads();
       constexpr int OWN = L::ROWS * R / AD_THREADS;
