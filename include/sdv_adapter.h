@@ -43,7 +43,8 @@ void sdv_adapters_destroy(sdv_adapters *adapters);
  *                      [row_offsets[b], row_offsets[b+1]).  Rows behind the last request's are not touched.
  *  adapter_ids [B] (device) the request's adapter, below `count`; negative: none, its rows of out are base's.
  *  x [T, k]            x_format 0 = bf16, 1 = fp32, rows x_stride elements apart.
- *  base, out [T, n]    y_format 0 = bf16, 1 = fp32; out may be base, else it overlaps neither base nor x.
+ *  base, out [T, n]    y_format 0 = bf16, 1 = fp32; out may be base, else it shares no memory with base; with x it never does
+ *                      (refused: SDV_ERR_INVALID_ARG; rows of unlike pitches have address ranges apart).
  * Pointers 16-byte aligned, strides multiples of 16 bytes.
  * out = base + scale * (x A^T) B^T: products of the values as they are (fp32 x as a sum of three bf16, the rank values of three for an
  * fp32 out and two for a bf16 one), sums in fp32, rounded once to out's format.  Infinities and NaN do what fp32 arithmetic does with

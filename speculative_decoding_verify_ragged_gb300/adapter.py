@@ -80,8 +80,8 @@ class Adapters:
 
     def apply(self, x, base, out, row_offsets, adapter_ids, status, stream=None):
         """out = base + scale (x A^T) B^T for the rows of each request under its adapter: x [T, K], base and out [T, N], bf16
-        or fp32 (base and out alike), rows strided; out may be base.  row_offsets [B + 1] and adapter_ids [B] int32, an id
-        below 0 being no adapter."""
+        or fp32 (base and out alike), rows strided; out may be base, and shares no memory with it or x otherwise.
+        row_offsets [B + 1] and adapter_ids [B] int32, an id below 0 being no adapter."""
         T = x.shape[0]
         xs = self._rows(x, "x", T, self.k, BOTH)
         bs, os_ = self._rows(base, "base", T, self.n, BOTH), self._rows(out, "out", T, self.n, (base.dtype,))

@@ -28,6 +28,7 @@
 
 #include "../../include/sdv_adapter.h"
 #include "chunk.cuh"
+#include "rows.h"
 
 namespace cg = cooperative_groups;
 
@@ -592,6 +593,11 @@ extern "C" sdv_status sdv_adapters_apply(sdv_adapters* h, const sdv_adapter_rows
       (r->base_stride * yb) % 16 || (r->out_stride * yb) % 16)
     return SDV_ERR_INVALID_ARG;
   if (r->out == r->base && r->out_stride != r->base_stride) return SDV_ERR_INVALID_ARG;
+  // base is read ahead of what is written, x by other blocks than write
+  const long long out_pitch = r->out_stride * yb, out_bytes = 1LL * h->cfg.n * yb;
+  if ((r->out != r->base && rows_share(r->out, out_pitch, out_bytes, r->base, r->base_stride * yb, out_bytes, r->T)) ||
+      rows_share(r->out, out_pitch, out_bytes, r->x, r->x_stride * xb, 1LL * h->cfg.k * xb, r->T))
+    return SDV_ERR_INVALID_ARG;
   AdapterParams p;
   p.r = *r;
   p.k = h->cfg.k;
