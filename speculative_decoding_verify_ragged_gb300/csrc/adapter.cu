@@ -72,7 +72,7 @@ __device__ __forceinline__ bool load_items(const AdapterParams& p, const Items& 
       if (b == p.r.B - 1) it.off[p.r.B] = e;
       it.id[b] = id;
       if (o < 0 || e < o || e > p.r.T || (b == 0 && o != 0) || id >= p.count) bad = 1;
-      else if (all || id >= 0) items = e - o > 8 ? static_cast<long long>((e - o + p.item_rows - 1) / p.item_rows) << 11 : e > o ? 1 : 0;
+      else if (all || id >= 0) items = e - o > 8 ? ((0LL + e - o + p.item_rows - 1) / p.item_rows) << 11 : e > o ? 1 : 0;
     }
     long long incl = items;
 #pragma unroll
@@ -531,7 +531,7 @@ cudaError_t start(AdapterParams p, int sms, cudaStream_t stream) {
   p.item_rows = L::ROWS == 64 && p.r.T >= 128LL * p.r.B ? 64 : 32;
   // items at most; a cluster as large as lets two in three of them run at once, two blocks to an SM: an item's time is mostly
   // waits, and many are short ones
-  const long long items = (p.r.T + p.item_rows - 1) / p.item_rows + (p.r.B < p.r.T ? p.r.B : p.r.T) - 1;
+  const long long items = (0LL + p.r.T + p.item_rows - 1) / p.item_rows + (p.r.B < p.r.T ? p.r.B : p.r.T) - 1;
   int cluster = MAX_CLUSTER;
   while (cluster > 2 && items * cluster > 3 * sms) cluster /= 2;
   const int most = 2 * sms / cluster * 4, clusters = static_cast<int>(items < most ? items : most);

@@ -38,3 +38,24 @@ def test_an_out_over_x_or_beside_base_is_refused():
     assert torch.equal(buf, before) and s["status"].item() == 0
     _apply(ad, s)
     _check(s, s["out"])
+
+
+@pytest.mark.parametrize("T", [2 ** 31 - 1, 2 ** 31 - 40])
+def test_buffers_of_the_most_rows(T):
+    """A launch planned for as many rows as the count holds; only the requests' rows are touched (columns of one buffer, so that no
+    rows are taken to overlap).  Items of 32 or 64 rows are counted past 32 bits on the way."""
+    import ctypes
+    from speculative_decoding_verify_ragged_gb300 import _abi
+    s = _make([3, 20, 1], [1, 0, -1], 64, 40, 16, 2, x="fp32", y="fp32", seed=6)
+    buf = torch.full((s["T"], 160), 3.0, device="cuda")
+    for k, at, n in (("x", 0, 64), ("base", 64, 40), ("out", 112, 40)):
+        view = buf[:, at:at + n]
+        view.copy_(s[k])
+        s[k] = view
+    ad = _adapters(s, max_rows=T)
+    r = _abi.SdvAdapterRows(3, T, s["row_offsets"].data_ptr(), s["adapter_ids"].data_ptr(), s["x"].data_ptr(), 1, 160, s["base"].data_ptr(),
+                            s["out"].data_ptr(), 1, 160, 160)
+    rc = ad.lib.sdv_adapters_apply(ad.handle, ctypes.byref(r), s["status"].data_ptr(), torch.cuda.current_stream().cuda_stream)
+    assert rc == 0
+    torch.cuda.synchronize()
+    _check(s, s["out"])
