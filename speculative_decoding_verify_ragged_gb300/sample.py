@@ -22,6 +22,8 @@ from ._abi import SdvSampleRows, load_library
 
 __all__ = ["sample"]
 
+INT_MAX = 2 ** 31 - 1
+
 
 def sample(logits, status, *, uniforms=None, tokens=None, probs=None, temperature=None, top_k=None, top_p=None, min_p=None,
            row_request=None, stream=None, lib=None):
@@ -62,10 +64,14 @@ def sample(logits, status, *, uniforms=None, tokens=None, probs=None, temperatur
     pp = None if top_p is None else _vector(top_p, "top_p", f32, requests, index)
     mp = None if min_p is None else _vector(min_p, "min_p", f32, requests, index)
     rp = None if row_request is None else _vector(row_request, "row_request", i32, rows, index)
+    if rows > INT_MAX or vocab > INT_MAX:
+        raise ValueError(f"logits: {tuple(logits.shape)}, sizes below 2^31 are wanted")
     if requests is None:
-        requests = rows if rp is None else 2 ** 31 - 1      # no setting is looked up
+        requests = rows if rp is None else INT_MAX          # no setting is looked up
     if rp is None and requests < rows:
         raise ValueError(f"settings of {requests} requests for {rows} rows: row_request says which a row takes")
+    if requests > INT_MAX:
+        requests = INT_MAX      # (what row_request can name)
     up = None if uniforms is None else _vector(uniforms, "uniforms", f32, rows, index)
     xp = None if tokens is None else _vector(tokens, "tokens", i32, rows, index)
     op = None
