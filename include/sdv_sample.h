@@ -42,8 +42,8 @@ extern "C" {
  * the shortest run whose sum of w = exp((z - max) / temperature) reaches top_p times theirs;
  * of those the ones with w >= min_p.  probs is w / (sum of those left), 0
  * elsewhere; the token is the first index whose running sum, by index, exceeds uniform * sum.
- * Both bounds are met on exact sums of integers: w in steps of 2^-42, within 2^-34 of itself down to 2^-13 and of the
- * largest below (what lies under 2^-43 of it adds nothing to a sum).  So which token is the last to stay, or the
+ * Both bounds are met on exact sums of integers: w in steps of 2^-42, within 2^-34 of itself down to 2^-13 of the
+ * largest and 2^-33 of the largest below (what lies under 2^-43 of it adds nothing to a sum).  So which token is the last to stay, or the
  * one drawn, does not depend on an order of summation.
  *
  * Device errors (SDV_ERR_BAD_INPUT): a setting or uniform out of range, a request

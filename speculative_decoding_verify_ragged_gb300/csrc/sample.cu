@@ -12,7 +12,7 @@
 // within 2^-34 of its value: t = (max - z) log2(e) / T is carried as an
 // unevaluated sum of two floats, its multiple of 2^-10 looked up (2^-j/1024, a table
 // of 1024 made from the series of exp) and the rest, below 2^-11, taken by a
-// quadratic.  Below 2^-13 the special-function unit's 2^-22, for the same t, is within 2^-34 of the largest.  Sums of integers
+// quadratic.  Below 2^-13 the special-function unit's 2^-22, for the same t, is within 2^-33 of the largest.  Sums of integers
 // are exact and have no order: any split over threads, blocks and passes gives the same answer.
 //
 // What can stay is nearly always a few hundred tokens of 10^5, so a row is read once and what may stay is
@@ -171,15 +171,18 @@ struct Weights {
     const u64 v = powers->fixed[j] + static_cast<long long>(__float2int_rn(__fmul_rn(powers->value[j], __fmul_rn(q, 4398046511104.f))));
     return n == 0 ? v : (v + (1ull << (n - 1))) >> n;
   }
-  // 2^-t in fp32.  Of what t lost, all but the difference's rounding is put right: that is t 2^-25 at most
-  __device__ __forceinline__ float rough(float z, float t, float scale) const {
+  // 2^-t in fp32 by the special-function unit (2^-22), `behind` being what t lost
+  static __device__ __forceinline__ float rough(float t, float behind, float scale) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(-t));
-    const float d = __fsub_rn(top, z);
-    return __fmul_rn(y, fmaf(fmaf(d, c_low, fmaf(d, c, -t)), -kLn2 * scale, scale));
+    return __fmul_rn(y, fmaf(behind, -kLn2 * scale, scale));
   }
-  // t from 13 on, below 2^29
-  __device__ __forceinline__ u32 coarse(float z, float t) const { return __float2uint_rn(rough(z, t, 4398046511104.f)); }
+  // t from 13 on, below 2^29.  Of what t lost, all but the difference's rounding is put right: that is t 2^-24 at most, with the rest 2^-33 of
+  // the largest weight at t = 13 and less beyond (all of it put right: rows without a setting 225 -> 240 us)
+  __device__ __forceinline__ u32 coarse(float z, float t) const {
+    const float d = __fsub_rn(top, z);
+    return __float2uint_rn(rough(t, fmaf(d, c_low, fmaf(d, c, -t)), 4398046511104.f));
+  }
   __device__ __forceinline__ u64 operator()(float z) const {
     const float t = t_of(z);
     if (!(t < 44.f)) return 0;  // below half a step; -inf
@@ -191,7 +194,7 @@ struct Weights {
     const float t = t_of(z);
     if (z == top) return 1.f;
     if (t < kFine) return static_cast<float>(fine(z, t)) * 0x1p-42f;
-    return t < 126.f ? rough(z, t, 1.f) : 0.f;
+    return t < 126.f ? rough(t, lost(z, t), 1.f) : 0.f;  // (at t = 126 the difference alone would be 2^-17.6 of it)
   }
 };
 

@@ -28,10 +28,9 @@ def _tile(x, rows):
 
 
 def _told(z, u, settings, tokens, probs):
-    """Rows against their definition in 64 bits.  The sum of weights is 2^-20 off at most: below 2^-13 of the largest a weight is 2^-22 off
-    by its exponential and t 2^-25 ln 2 by its difference (t = 40: 2^-20.2, of what little lies there).  So a bound nearer than that to a
-    token's end may take it or leave it, and likewise the token drawn."""
-    e = 2.0 ** -20
+    """Rows against their definition in 64 bits.  Below 2^-13 of the largest (t = 13) a weight is off by its exponential and two roundings,
+    2^-22 + 2^-23, and by the difference's in t, t 2^-24 ln 2; above by 2^-34, and all by half a step of 2^-42.  What that comes to of the
+    row's sum is how far a bound may lie from a token's end and take it or leave it, and likewise the token drawn."""
     d = dict(temperature=1.0, top_k=0, top_p=1.0, min_p=0.0)
     st = {n: settings[n].double().tolist() if n in settings else [v] * z.shape[0] for n, v in d.items()}
     for r in range(z.shape[0]):
@@ -43,6 +42,9 @@ def _told(z, u, settings, tokens, probs):
             order = order[: 1 if t == 0.0 else int(k)]
         v = x[order]
         w = torch.where(v == v[0], 0.0, (v - v[0]) / (t or 1.0)).exp()
+        bits = torch.where(v == v[0], 0.0, (v[0] - v) / (t or 1.0) * 1.442695).clamp(max=64.0)
+        e = (w * torch.where(bits < 13.0, 2.0 ** -34, bits * 2.0 ** -24 * 0.6932 + 2.0 ** -22 + 2.0 ** -23)).sum().item() / w.sum().item()
+        e += v.numel() * 2.0 ** -43
         got = int((probs[r] > 0).sum())
         n = order.numel()
         if p < 1.0 and t > 0.0:
@@ -119,7 +121,7 @@ def test_bounds_about_the_ends_of_tokens(rows, temperature):
     c = float(np.float32(temperature))
     w = (z.double()[0] / c).softmax(0)
     t = (z.double().max() - z.double()[0]) / c * 1.442695
-    assert (w * (t * 2.0 ** -25 * 0.6932 + 2.0 ** -22)).sum().item() < 2.0 ** -20
+    assert (w * torch.where(t < 13.0, 2.0 ** -34, t * 2.0 ** -24 * 0.6932 + 2.0 ** -22 + 2.0 ** -23)).sum().item() < 2.0 ** -20
     order = torch.argsort(w, descending=True, stable=True)
     reach = w[order].cumsum(0)
     ps = []
