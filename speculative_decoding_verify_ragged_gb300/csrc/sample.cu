@@ -35,7 +35,7 @@
 // Bound by the row's bytes where rows are many, by waits one after another (settings, first loads, the sample, meetings, the
 // list) where they are few: 512 rows of 151936 fp32 values under top-p (311 MB) 99 us, 3.1 TB/s: while it reads, a
 // block keeps pace with memory, but some 8 us of waits a block lie beside 25 us of reading, and 512 blocks are 1.7 of what
-// runs at once; greedy 68 us, top-k 83, no setting (two readings, every weight) 213; one row 9 to 20 us.
+// runs at once; greedy 69 us, top-k 83, no setting (two readings, every weight) 224; one row 9 to 20 us.
 #include <atomic>
 
 #include <cooperative_groups.h>
@@ -1200,7 +1200,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
       if (sums) others = warp_sum(lane < blocks && theirs->block_rest > 0.f ? theirs->block_rest * exp2f((theirs->block_ref - top) * c) : 0.f);
       // in steps of 2^-42.  Its error, up to t = 32: of t a difference, a product, the quotient log2(e) / T (2^-24 each) and log2(e) itself
       // (2^-26), alike for the scale to `top`, 1.7 * 2^-23 of t in all, so 2^-17.7 of a term; 2^-22 of each exponential; 2^-16 of a
-      // thread's sums of up to 250 terms: below 2^-15 together.  Beyond t = 32 2^20 tokens add up to 2^-12 of the largest weight at
+      // thread's sums of up to 250 terms; and 2^-19.4 of the weights that it stands for: below 2^-15 together.  Beyond t = 32 2^20 tokens add up to 2^-12 of the largest weight at
       // most, with errors of 2^-16: 2^-28.  What the sum stands for has each token rounded to a step, half of one away at most.
       const u64 sum = static_cast<u64>(others * 4398046511104.f);
       const u64 off = (sum >> 15) + (1 << 14) + p.r.vocab / 2;
@@ -1241,8 +1241,10 @@ template <typename T>
 cudaError_t launch(const sdv_sample_rows& rows, int* status, int device, int sms, cudaStream_t stream) {
   constexpr int N = Word<T>::N;
   const int words = rows.vocab / N + 2;  // at most, wherever the row begins
-  // more blocks to a row where they all run at once (two to an SM), and runs of at most 1000 values a thread.  A block costs some 8 us
-  // beside its run, and clusters of 4 and 8 do not fill the SMs.  Rows x values (fp32): us with 1, 2, 4 and 8 blocks
+  // more blocks to a row while they are few for the SMs, and runs of at most 1000 values a thread.  A block costs some 8 us beside its run;
+  // two run on an SM, so pairs may be a little more than run at once (11 / 4 to an SM), fours as many (2) and eights half of that, as
+  // clusters of 8 leave SMs unfilled.  The three limits stand between these measured points; nothing was measured nearer to them, and
+  // rows that row_request turns off count as rows.  Rows x values (fp32): us with 1, 2, 4 and 8 blocks
   //   512 x 151936, top-p       107  128 174 310      64 x 151936, mixed settings  81  51  41  62
   //   200 x 50000, distributions 173 64 112 167     40 x 20011, no setting       25  21  15  21
   int blocks = 1;
