@@ -21,6 +21,7 @@ from .cache import _c_int
 __all__ = ["Adapters"]
 
 BOTH = (torch.bfloat16, torch.float32)
+INT_MAX = 2 ** 31 - 1
 
 
 class Adapters:
@@ -93,7 +94,9 @@ class Adapters:
         if status.dtype is not torch.int32 or status.get_device() != self._index:
             raise ValueError(f"status: {status.dtype} on {status.device}, int32 on {self.device} is wanted")
         raw = torch._C._cuda_getCurrentRawStream(self._index) if stream is None else stream.cuda_stream
-        r = SdvAdapterRows(_c_int(B), _c_int(T), row_offsets.data_ptr(), adapter_ids.data_ptr(), x.data_ptr(), 1 if x.dtype is torch.float32 else 0, xs,
+        if T > INT_MAX or B > INT_MAX:
+            raise ValueError(f"x: {tuple(x.shape)}, adapter_ids: {tuple(adapter_ids.shape)}, sizes below 2^31 are wanted")
+        r = SdvAdapterRows(B, T, row_offsets.data_ptr(), adapter_ids.data_ptr(), x.data_ptr(), 1 if x.dtype is torch.float32 else 0, xs,
                            base.data_ptr(), out.data_ptr(), 1 if base.dtype is torch.float32 else 0, bs, os_)
         rc = self.lib.sdv_adapters_apply(self.handle, ctypes.byref(r), status.data_ptr(), raw)
         if rc:

@@ -9,7 +9,7 @@ STREAM = types.SimpleNamespace(cuda_stream=0)
 
 
 def test_rows_of_the_adapters_are_not_wrapped():
-    """The library, a recorder here, sees the largest count there is, and refuses it."""
+    """The library is a recorder here."""
     from speculative_decoding_verify_ragged_gb300 import adapter
     from speculative_decoding_verify_ragged_gb300._abi import SdvAdapterRows
     seen = []
@@ -18,10 +18,16 @@ def test_rows_of_the_adapters_are_not_wrapped():
                                    sdv_adapters_destroy=lambda h: None)
     ad.handle, ad._index, ad.device, ad.k, ad.n = 1, -1, torch.device("cpu"), 8, 16
     i32 = dict(dtype=torch.int32)
-    for rows, want in ((4, 4), (2 ** 31 - 1, 2 ** 31 - 1), (2 ** 31, 2 ** 31 - 1), (2 ** 32 + 4, 2 ** 31 - 1)):
+    for rows in (4, 2 ** 31 - 1, 2 ** 31, 2 ** 32 + 4):
         x, y = torch.zeros((1, 8)).expand(rows, 8), torch.zeros((1, 16)).expand(rows, 16)
-        ad.apply(x, y, y, torch.zeros(2, **i32), torch.zeros(1, **i32), torch.zeros(1, **i32), stream=STREAM)
-        assert seen[-1] == want
+        call = lambda: ad.apply(x, y, y, torch.zeros(2, **i32), torch.zeros(1, **i32), torch.zeros(1, **i32), stream=STREAM)  # noqa: E731
+        if rows < 2 ** 31:
+            call()
+            assert seen[-1] == rows
+        else:
+            with pytest.raises(ValueError, match="2\\^31"):
+                call()
+    assert len(seen) == 2
 
 
 @pytest.mark.gpu
