@@ -6,7 +6,7 @@
 // that of one request after another.
 //
 // A few bytes, so all latency: launch, the lengths, three sums, the moved pages, the rows, one after another.  One request 4.9 us, 64
-// requests with 2800 rows and 3900 moved pages 6.9 us, 1024 with 18900 and 37000 12.8 us (one block alone: 9.2 and 41 us).
+// requests with 2800 rows and 3900 moved pages 7.0 us, 1024 with 18900 and 37000 12.9 us (one block alone: 9.2 and 41 us).
 #include <cooperative_groups.h>
 
 #include "chunk.cuh"
