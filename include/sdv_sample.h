@@ -45,7 +45,7 @@ extern "C" {
  * Both bounds are met on exact sums of integers: w in steps of 2^-42, within 2^-34 of itself down to 2^-13 of the
  * largest and 2^-33 of the largest below (what lies under 2^-43 of it adds nothing to a sum).  So which token is the last to stay, or the
  * one drawn, does not depend on an order of summation.
- * probs is that quotient in fp32, within 2^-20.8 of itself, and 0 for tokens below 2^-126 of the largest, though they stay.
+ * probs is that quotient in fp32, within 2^-20.8 of itself or 2^-149, and 0 for tokens below 2^-126 of the largest, though they stay.
  *
  * Device errors (SDV_ERR_BAD_INPUT): a setting or uniform out of range, a request
  * not below `requests`, a row with a NaN or with nothing above -inf. */
